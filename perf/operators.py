@@ -186,9 +186,8 @@ def prepare(case, seed):
         dt = DTYPES[case["dtype"]]
         # gradients of very unequal size, as A's and B's are
         s["grads"] = [normal(a, b, std=3e-4 * (1 + i % 5), dtype=dt) for i, (a, b) in enumerate(_adapters(case))]
-        # the optimizer's flat buffer that takes them, and its views
+        # the optimizer's flat buffer that takes them, one after the other
         s["flat"] = torch.empty(sum(t.numel() for t in s["grads"]), dtype=dt, device="cuda")
-        s["out"] = [t.reshape(g.shape) for t, g in zip(s["flat"].split([t.numel() for t in s["grads"]]), s["grads"])]
         return s
     if case["op"].startswith("norm"):
         dt = DTYPES[case["dtype"]]
@@ -344,7 +343,7 @@ def run(state):
         if op == "norm_bwd":
             dx, dw, db = qn.norm_bwd(s["dy"], s["x"], s["weight"], s["mean"], s["rstd"], rms=case["rms"])
             return {"dx": dx, "dw": dw} if case["rms"] else {"dx": dx, "dw": dw, "db": db}
-        norm = qn.clip_grad_norm(s["grads"], case["max_norm"], out=s["out"])
+        norm = qn.clip_grad_norm(s["grads"], case["max_norm"], out=s["flat"])
         return {"norm": norm, "grads": s["flat"]}
     if op == "attn_fwd":
         o, lse = _plain_attn_fwd(s)
