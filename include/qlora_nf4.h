@@ -447,6 +447,136 @@ int32_t qlora_ilp_plan(int32_t n_matrices, int32_t n_configs, const double* err,
                        const int64_t* bytes, int64_t budget, int32_t* choice,
                        double* total_err, int64_t* total_bytes);
 
+/* ---- Around the layer: attention, norms, gradient clipping ----
+ *
+ * The other operators of a finetuning step.  Element types of the norms and
+ * of the clipping: QLORA_TYPE_BF16 or QLORA_TYPE_FP32 (others give
+ * QLORA_ERR_UNSUPPORTED).  Attention is bf16 with fp32 sums. */
+#define QLORA_TYPE_BF16 0
+#define QLORA_TYPE_FP32 1
+
+/* One [batch, row, head, dim] bf16 tensor: device pointer (16-byte aligned)
+ * and element strides; the dim stride is 1.  Strides must be multiples of 8,
+ * not negative, and the row stride at most QLORA_ATTN_MAX_STRIDE.  q, k and v
+ * may be views of one projection's output; strides of 0 are allowed for
+ * inputs.  The batch stride is not used for packed batches. */
+#define QLORA_ATTN_MAX_STRIDE ((int64_t)1 << 22)
+typedef struct qlora_heads_t {
+  uint16_t* data;
+  int64_t batch_stride, row_stride, head_stride;
+} qlora_heads_t;
+
+/* What is attended to what.
+ *   Dense: cu_seqlens_q = cu_seqlens_k = NULL; n_seq sequences of q_rows
+ *   queries and k_rows keys each.
+ *   Packed: q_rows and k_rows are the rows of all n_seq sequences together;
+ *   cu_seqlens_q / _k (device, int32, n_seq + 1 ascending offsets from 0;
+ *   both given, equal pointers for self-attention): sequence s has the query
+ *   rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1 and likewise the keys.
+ *   Sequences may be empty on either side.  Rows past the last offset belong
+ *   to no sequence: they are not read, and outputs there are 0 (lse -inf).
+ *   The offsets are read by the kernels and clamped to the rows, so wrong
+ *   ones give undefined outputs but no access outside the tensors.
+ *   Causal: query i of a sequence of lq queries and lk keys sees the keys
+ *   j <= i + lk - lq (the last query sees the last key).
+ * Each key/value head serves heads / kv_heads consecutive query heads. */
+typedef struct qlora_attention_t {
+  int64_t n_seq;
+  int64_t q_rows, k_rows;       /* >= 0, below 2^30 */
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int32_t heads, kv_heads;      /* kv_heads divides heads */
+  int32_t head_dim;             /* a multiple of 8 up to QLORA_ATTN_MAX_DIM
+                                   (others: QLORA_ERR_UNSUPPORTED) */
+  int32_t causal;
+  float scale;                  /* > 0, finite */
+} qlora_attention_t;
+#define QLORA_ATTN_MAX_DIM 128
+
+/* qlora_attention_fwd -- per head O = softmax(scale Q K^T) V over the keys
+ * that each query sees, and lse = log sum exp(scale q k) of each row (fp32,
+ * natural logarithm; dense [n_seq, heads, q_rows], packed [heads, q_rows]).
+ * A query that sees no key gets O = 0 and lse = -inf.  Sums and the softmax
+ * are fp32; the probabilities are rounded to bf16 for the product with V.
+ * Values outside a sequence never reach its outputs, whatever they are; a
+ * NaN or infinity inside one may reach every row of that sequence and head. */
+int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
+                            const qlora_heads_t* k, const qlora_heads_t* v,
+                            const qlora_heads_t* o, float* lse, hipStream_t stream);
+
+/* qlora_attention_bwd -- the gradients of q, k and v for the output gradient
+ * dout, with the probabilities recomputed from lse (o and lse as the forward
+ * wrote them):
+ *   P = exp(scale Q K^T - lse),  dS = P (dO V^T - rowsum(dO O)),
+ *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+ * dK and dV summed over the query heads of a key/value head.  dq, dk and dv
+ * are overwritten; queries that see no key, and keys that no query sees, get
+ * 0.  P and dS are rounded to bf16 for the products that follow.
+ * ws_bytes >= qlora_attention_bwd_workspace_size(a) (0 for invalid sizes or
+ * no queries; ws may then be NULL). */
+size_t qlora_attention_bwd_workspace_size(const qlora_attention_t* a);
+int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
+                            const qlora_heads_t* k, const qlora_heads_t* v,
+                            const qlora_heads_t* o, const float* lse,
+                            const qlora_heads_t* dout, const qlora_heads_t* dq,
+                            const qlora_heads_t* dk, const qlora_heads_t* dv, void* ws,
+                            size_t ws_bytes, hipStream_t stream);
+
+/* qlora_norm_fwd -- layer norm (rms = 0) or root-mean-square norm (rms = 1) of
+ * each row of x [rows, width]:
+ *   mean = sum(x) / width (0 if rms),  rstd = 1 / sqrt(sum((x - mean)^2) / width + eps),
+ *   y = (x - mean) rstd weight + bias.
+ *   x, y          [rows, width] of x_type, 0 <= rows < 2^30, 1 <= width <=
+ *                 QLORA_NORM_MAX_WIDTH_BF16 / _FP32 by x_type (more:
+ *                 QLORA_ERR_UNSUPPORTED)
+ *   weight, bias  [width] of w_type; bias may be NULL
+ *   mean, rstd    [rows] fp32 out; mean may be NULL if rms
+ * These pointers need the alignment of their elements only.  eps >= 0. */
+#define QLORA_NORM_MAX_WIDTH_BF16 65536
+#define QLORA_NORM_MAX_WIDTH_FP32 32768
+int32_t qlora_norm_fwd(const void* x, int64_t rows, int64_t width, int32_t x_type,
+                       const void* weight, const void* bias, int32_t w_type, float eps,
+                       int32_t rms, void* y, float* mean, float* rstd, hipStream_t stream);
+
+/* qlora_norm_bwd -- its gradients, from x, the row statistics and dy:
+ *   z = (x - mean) rstd,  g = dy weight,
+ *   dx = rstd (g - z mean(g z) - [mean(g) unless rms]),
+ *   dweight = sum over rows of dy z,  dbias = sum over rows of dy.
+ * dx [rows, width] of x_type; dweight, dbias [width] of w_type, summed in
+ * fp32.  Each of the three may be NULL (skipped).  Outputs are overwritten.
+ * ws_bytes >= qlora_norm_bwd_workspace_size(rows, width, x_type) (16-byte
+ * aligned; 0 for invalid sizes; not used without dweight and dbias). */
+size_t qlora_norm_bwd_workspace_size(int64_t rows, int64_t width, int32_t x_type);
+int32_t qlora_norm_bwd(const void* dy, const void* x, int64_t rows, int64_t width,
+                       int32_t x_type, const void* weight, int32_t w_type, int32_t rms,
+                       const float* mean, const float* rstd, void* dx, void* dweight,
+                       void* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* qlora_clip_grad_norm -- the 2-norm of n gradient tensors taken together,
+ * and their scaling by min(1, max_norm / (norm + 1e-6)).
+ *   n          tensors, 0 <= n <= 2^20
+ *   grads      HOST array of n device pointers (aligned to their elements)
+ *   sizes      HOST array: elements of each (0 allowed; 2^44 in all)
+ *   types      HOST array: QLORA_TYPE_* of each
+ *   max_norm   >= 0 (not NaN); +inf never scales
+ *   out        HOST array of n device pointers that take the scaled gradients
+ *              (same sizes and types; each either its gradient itself or
+ *              apart from all of them), or NULL: in place.  In place, nothing
+ *              is written when the factor is 1.
+ *   norm       one float (device) out, the norm before scaling
+ * The three arrays are read during the call and not kept.  Squares are summed
+ * in fp64.  A NaN norm scales by NaN, an infinite one by 0, as
+ * min(1, max_norm / (norm + 1e-6)) says.  ws: 16-byte aligned device memory of
+ * qlora_clip_workspace_size(n) bytes.
+ * qlora_grad_norm is the norm alone. */
+size_t qlora_clip_workspace_size(int64_t n);
+int32_t qlora_clip_grad_norm(int64_t n, const void* const* grads, const int64_t* sizes,
+                             const int32_t* types, float max_norm, void* const* out,
+                             float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
+int32_t qlora_grad_norm(int64_t n, const void* const* grads, const int64_t* sizes,
+                        const int32_t* types, float* norm, void* ws, size_t ws_bytes,
+                        hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,6 +31,9 @@ QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 # Workgroups (and sink words) of qlora_stream_read
 QLORA_STREAM_GRID = 1024
 
+QLORA_TYPE_BF16 = 0
+QLORA_TYPE_FP32 = 1
+
 # Every symbol the header declares.
 EXPORTS = (
     "qlora_status_str",
@@ -58,6 +61,15 @@ EXPORTS = (
     "qlora_config_bytes",
     "qlora_config_error_workspace_size",
     "qlora_config_error",
+    "qlora_attention_fwd",
+    "qlora_attention_bwd",
+    "qlora_attention_bwd_workspace_size",
+    "qlora_norm_fwd",
+    "qlora_norm_bwd",
+    "qlora_norm_bwd_workspace_size",
+    "qlora_clip_workspace_size",
+    "qlora_clip_grad_norm",
+    "qlora_grad_norm",
 )
 
 
@@ -73,6 +85,32 @@ class Nf4Tensor(ctypes.Structure):
         ("dq_blocksize", ctypes.c_int32),
         ("code_type", ctypes.c_int32),
         ("levels", ctypes.c_void_p),
+    ]
+
+
+class Heads(ctypes.Structure):
+    """Mirror of qlora_heads_t."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("batch_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class Attention(ctypes.Structure):
+    """Mirror of qlora_attention_t."""
+    _fields_ = [
+        ("n_seq", ctypes.c_int64),
+        ("q_rows", ctypes.c_int64),
+        ("k_rows", ctypes.c_int64),
+        ("cu_seqlens_q", ctypes.c_void_p),
+        ("cu_seqlens_k", ctypes.c_void_p),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -149,6 +187,26 @@ def lib() -> ctypes.CDLL:
     L.qlora_config_error.argtypes = [vp, i64, i64, i32, i32, vp, vp, i32, vp, vp, sz, vp]
     L.qlora_ilp_plan.restype = i32
     L.qlora_ilp_plan.argtypes = [i32, i32, vp, vp, i64, vp, vp, vp]
+    pa, ph = ctypes.POINTER(Attention), ctypes.POINTER(Heads)
+    L.qlora_attention_fwd.restype = i32
+    L.qlora_attention_fwd.argtypes = [pa, ph, ph, ph, ph, vp, vp]
+    L.qlora_attention_bwd_workspace_size.restype = sz
+    L.qlora_attention_bwd_workspace_size.argtypes = [pa]
+    L.qlora_attention_bwd.restype = i32
+    L.qlora_attention_bwd.argtypes = [pa, ph, ph, ph, ph, vp, ph, ph, ph, ph, vp, sz, vp]
+    L.qlora_norm_fwd.restype = i32
+    L.qlora_norm_fwd.argtypes = [vp, i64, i64, i32, vp, vp, i32, f32, i32, vp, vp, vp, vp]
+    L.qlora_norm_bwd_workspace_size.restype = sz
+    L.qlora_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
+    L.qlora_norm_bwd.restype = i32
+    L.qlora_norm_bwd.argtypes = [vp, vp, i64, i64, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz,
+                                 vp]
+    L.qlora_clip_workspace_size.restype = sz
+    L.qlora_clip_workspace_size.argtypes = [i64]
+    L.qlora_clip_grad_norm.restype = i32
+    L.qlora_clip_grad_norm.argtypes = [i64, vp, vp, vp, f32, vp, vp, vp, sz, vp]
+    L.qlora_grad_norm.restype = i32
+    L.qlora_grad_norm.argtypes = [i64, vp, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 

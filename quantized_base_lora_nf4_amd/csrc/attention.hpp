@@ -1,0 +1,314 @@
+// What the attention kernels share: which sequence, head and tile a
+// workgroup works on, K/V (or Q/dO) tiles in LDS, and the MFMA fragments.
+//
+// Matrix products.  Every product has one operand in registers for the whole
+// kernel or fresh from the previous product (the B operand: column index =
+// lane % 32), and one that comes from a tile in LDS (the A operand).  A
+// wave owns 32 columns: query rows in the forward and the dQ kernel, keys
+// in the dK/dV kernel.  The score tile is computed with the tile's rows as
+// the MFMA's row index, so that the probabilities come out as
+// "column = lane % 32, rows in registers", which is what the following
+// product takes as its B operand; nothing goes through LDS in between.  An
+// MFMA 32x32 result holds row 8 a + 4 h + c in element 4 a + c of half h =
+// lane / 32, while the B operand of the next one wants rows 8 h + e of each
+// 16-row slab in elements e = 0..7; reading tile row swap23(i) as A row i
+// (bits 2 and 3 exchanged) makes the two agree.  The same exchange on the
+// output columns leaves 8 consecutive output elements in a lane, so
+// results are stored 16 bytes at a time.
+//
+// Tiles in LDS are [64][DP] bf16, DP = 64 or 128 (the head dimension rounded
+// up; dimensions past D hold copies of valid ones, meet zeros in the
+// register operand, and are not stored).  The 16-byte chunks of a row are
+// stored in the order chunk ^ mask(row), chosen so that both ways of
+// reading are free of bank conflicts: 16 rows of one chunk (ds_read_b128)
+// and 4 + 4 rows of 4 chunks (the transposing ds_read_b64_tr_b16).
+#pragma once
+
+#include "kernels.hpp"
+
+namespace qn {
+namespace attn {
+
+constexpr int kTile = 64;    // rows of a tile in LDS
+constexpr int kWaves = 4;    // waves per workgroup
+constexpr int kCols = 32;    // columns per wave
+constexpr int kBlock = kWaves * kCols;  // columns per workgroup
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_inff();
+
+// ---- which tile ----
+
+// One workgroup's work: `tile` of the columns of one sequence.
+struct Work {
+  int head;
+  int64_t batch;           // dense: batch index (packed: 0)
+  int64_t q0, k0;          // first query and key row of the sequence (packed; dense: 0)
+  int lq, lk;              // lengths
+  int tile, ntiles;        // tile of kBlock columns, and how many the sequence has
+  bool valid;
+};
+
+// Workgroups go to the 8 XCDs round-robin by id, and each XCD has its own
+// L2: a contiguous range of work per XCD keeps the tiles of one head, and the
+// heads that share K and V, on one L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t p, int64_t total) {
+  const int64_t per = total >> 3;
+  if (p >= per * 8) return p;
+  return (p & 7) * per + (p >> 3);
+}
+
+__device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
+  return (int)(v < lo ? lo : v > hi ? hi : v);
+}
+
+// Dense: every sequence has the same tiles, ntiles = ceil(cols / kBlock).
+// Packed: `slots` tiles per head, at least as many as all sequences have;
+// the tile's sequence is found from the lengths (64 at a time, by a prefix
+// sum over the wave).  After the last sequence, the rows that belong to
+// none form one more, with nothing on the other side, so that outputs are
+// zero there.  Offsets are clamped to the tensors' rows, so that wrong
+// ones give wrong results but no access out of range.
+// kKeys: the columns are keys (the dK/dV kernel), else queries.
+template <bool kKeys>
+__device__ __forceinline__ Work find_work(const AttnArgs& p, int64_t id, int64_t slots,
+                                          int heads) {
+  Work w;
+  w.head = (int)((id / slots) % heads);
+  const int64_t slot = id % slots;
+  if (!p.cu_q) {
+    w.batch = id / slots / heads;
+    w.q0 = w.k0 = 0;
+    w.lq = (int)p.Sq;
+    w.lk = (int)p.Sk;
+    w.tile = (int)slot;
+    w.ntiles = (int)slots;
+    w.valid = true;
+    return w;
+  }
+  w.batch = 0;
+  w.valid = false;
+  const int lane = threadIdx.x & 63;
+  const int32_t* cu = kKeys ? p.cu_k : p.cu_q;
+  const int64_t rows = kKeys ? p.Sk : p.Sq;
+  int64_t base = 0;
+  for (int s0 = 0; s0 <= p.nseq; s0 += 64) {
+    const int s = s0 + lane;
+    int n = 0;
+    if (s <= p.nseq) {
+      const int64_t a = clamp_row(cu[s], 0, rows);
+      const int64_t b = s < p.nseq ? clamp_row(cu[s + 1], a, rows) : rows;
+      n = (int)((b - a + kBlock - 1) / kBlock);
+    }
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += up;
+    }
+    const uint64_t past = __ballot(base + sum > slot);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int sq = __builtin_amdgcn_readfirstlane(s0 + l);
+      w.ntiles = __builtin_amdgcn_readfirstlane(__shfl(n, l, 64));
+      w.tile = (int)(slot - base) - __builtin_amdgcn_readfirstlane(__shfl(sum - n, l, 64));
+      const bool none = sq == p.nseq;
+      w.q0 = clamp_row(p.cu_q[sq], 0, p.Sq);
+      w.k0 = clamp_row(p.cu_k[sq], 0, p.Sk);
+      const int qe = none ? (kKeys ? (int)w.q0 : (int)p.Sq) : clamp_row(p.cu_q[sq + 1], w.q0, p.Sq);
+      const int ke = none ? (kKeys ? (int)p.Sk : (int)w.k0) : clamp_row(p.cu_k[sq + 1], w.k0, p.Sk);
+      w.lq = qe - (int)w.q0;
+      w.lk = ke - (int)w.k0;
+      w.valid = true;
+      return w;
+    }
+    base += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return w;
+}
+
+// Tiles per head to launch for `cols` columns.
+inline int64_t tile_slots(const AttnArgs& a, int64_t cols) {
+  const int64_t n = (cols + kBlock - 1) / kBlock;
+  return a.cu_q ? cols / kBlock + a.nseq + 1 : (n > 0 ? n : 1);
+}
+
+// ---- tiles in LDS ----
+
+template <int DP>
+struct Geo {
+  static constexpr int kChunks = DP / 8;           // 16-byte chunks per row
+  static constexpr int kElems = kTile * DP;        // elements of a tile
+  static constexpr int kSteps = DP / 16;           // 16-deep contraction steps over the dimension
+  static constexpr int kDT = DP / 32;              // 32-wide tiles of the dimension
+  // 16-byte loads per thread that fill a tile
+  static constexpr int kLoads = kTile * kChunks / (kWaves * 64);
+};
+
+// Chunk mask of a row (see above).
+template <int DP>
+__device__ __forceinline__ int chunk_mask(int row) {
+  if constexpr (DP == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+}
+
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
+// The per-lane byte offsets of this wave's loads of a tile: load i fills
+// 1024 consecutive bytes of LDS (64 / kChunks rows), lane l's 16 bytes at
+// 16 l, so the lane fetches the chunk that the mask puts there.  Rows past
+// the last one read the last row again, chunks past D the row's first.
+template <int DP>
+struct TileLoader {
+  int row[Geo<DP>::kLoads];   // tile row
+  int cols[Geo<DP>::kLoads];  // byte offset within the row
+};
+
+template <int DP>
+__device__ __forceinline__ void tile_loader(TileLoader<DP>& t, int D, int wave, int lane) {
+  constexpr int C = Geo<DP>::kChunks, R = 64 / C;
+#pragma unroll
+  for (int i = 0; i < Geo<DP>::kLoads; ++i) {
+    const int r = (i * kWaves + wave) * R + lane / C;
+    const int c = (lane % C) ^ chunk_mask<DP>(r);
+    t.row[i] = r;
+    t.cols[i] = c * 8 < D ? c * 16 : 0;
+  }
+}
+
+// Issues the loads of rows row0 .. row0 + 63 (clamped to nrows - 1) of the
+// matrix at base (row stride st elements) into the tile at `lds`.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint16_t* lds, const TileLoader<DP>& t,
+                                          const uint16_t* base, int64_t st, int row0, int nrows,
+                                          int wave) {
+  const int left = nrows - row0;  // >= 1
+  const int64_t bytes = ((int64_t)((left < kTile ? left : kTile) - 1) * st + DP) * 2;
+  const __amdgpu_buffer_rsrc_t rsrc =
+      bytes_rsrc(base + (int64_t)row0 * st, bytes < 0x7fffffff ? bytes : 0x7fffffff);
+#pragma unroll
+  for (int i = 0; i < Geo<DP>::kLoads; ++i) {
+    const int r = t.row[i] < left ? t.row[i] : left - 1;
+    const int voff = r * (int)(st * 2) + t.cols[i];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void*)(lds + (i * kWaves + wave) * 512), 16, voff,
+        0, 0, 0);
+  }
+}
+
+// This wave's tile loads have landed, and every wave is here.
+__device__ __forceinline__ void tiles_ready() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ---- fragments ----
+
+__device__ __forceinline__ int swap23(int r) {
+  return (r & ~12) | ((r & 4) << 1) | ((r & 8) >> 1);
+}
+
+// A lane's offset (elements) of its fragments within a tile.  The dimension
+// steps only change bits of the chunk index that nothing else adds to, so
+// they are exclusive-ored into one base per kind of read.
+struct FragOff {
+  int row;  // rows as A rows
+  int tr;   // transposed
+};
+
+// Transposed reads: A row i of the fragment is dimension swap23(i) of a
+// 32-wide slab, its 16 contraction entries are tile rows.  Within each group
+// g of 16 lanes, lane j reads 4 consecutive dimensions of row
+// 8 (g / 2) + j / 4 (+ 4 in the second read) and receives 4 consecutive rows
+// of the dimension that A row 16 (g % 2) + j stands for.
+template <int DP>
+__device__ __forceinline__ FragOff frag_off(int lane) {
+  FragOff f;
+  const int r = swap23(lane & 31);
+  f.row = r * DP + (((lane >> 5) ^ chunk_mask<DP>(r)) << 3);
+  const int g = lane >> 4, j = lane & 15;
+  const int x = 4 * (g & 1) + (j & 3);                       // which 4 A rows
+  const int x4 = (x & 4) | ((x & 1) << 1) | ((x >> 1) & 1);  // the 4 dimensions they stand for
+  const int rt = 8 * (g >> 1) + (j >> 2);
+  f.tr = rt * DP + (((x4 >> 1) ^ chunk_mask<DP>(rt)) << 3) + 4 * (x4 & 1);
+  return f;
+}
+
+// Tile rows 32 rt + swap23(lane % 32), dimensions 16 s + 8 (lane / 32) + 0..7.
+template <int DP>
+__device__ __forceinline__ bf16x8 read_rows(const uint16_t* tile, const FragOff& f, int s, int rt) {
+  return *reinterpret_cast<const bf16x8*>(tile + (f.row ^ (s << 4)) + rt * 32 * DP);
+}
+
+// Tile rows 16 slab + 8 (lane / 32) + 0..7 of dimension 32 d + swap23(lane % 32).
+template <int DP>
+__device__ __forceinline__ bf16x8 read_tr(const uint16_t* tile, const FragOff& f, int d, int slab) {
+  typedef short v4i16 __attribute__((ext_vector_type(4)));
+  typedef short v8i16 __attribute__((ext_vector_type(8)));
+  typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+  const int o = f.tr ^ (d << 5);
+  // the row 4 further on has the lowest bit of its chunk mask flipped
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(tile + o + slab * 16 * DP));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds_v4i16*)(tile + (o ^ 8) + slab * 16 * DP + 4 * DP));
+  const v8i16 v = v8i16{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// The register operand: row `r` (per lane) of a matrix, dimensions
+// 16 s + 8 (lane / 32) + 0..7 in element s, zeros past D.
+template <int DP>
+__device__ __forceinline__ void load_cols(bf16x8 (&f)[Geo<DP>::kSteps], const uint16_t* row, int D,
+                                          int lane) {
+#pragma unroll
+  for (int s = 0; s < Geo<DP>::kSteps; ++s) {
+    const int d = 16 * s + 8 * (lane >> 5);
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    f[s] = as_bf16x8(d < D ? *reinterpret_cast<const u32x4*>(row + d) : z);
+  }
+}
+
+// Stores a [dimension][column] accumulator: this lane's column is the row
+// `out` of the output, times `mul`.
+template <int DP>
+__device__ __forceinline__ void store_cols(uint16_t* out, const f32x16 (&acc)[Geo<DP>::kDT],
+                                           float mul, int D, int lane) {
+#pragma unroll
+  for (int t = 0; t < Geo<DP>::kDT; ++t)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const int d = 32 * t + 16 * a + 8 * (lane >> 5);
+      if (d < D) {
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = pack_bf16x2(acc[t][8 * a + 2 * e] * mul, acc[t][8 * a + 2 * e + 1] * mul);
+        *reinterpret_cast<u32x4*>(out + d) = v;
+      }
+    }
+}
+
+// Elements 8 s .. 8 s + 7 of a score accumulator as the B operand of a
+// 16-deep product.
+__device__ __forceinline__ bf16x8 pack8(const f32x16& x, int s) {
+  u32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(x[8 * s + 2 * e], x[8 * s + 2 * e + 1]);
+  return as_bf16x8(v);
+}
+
+// Tile row of element v of a score accumulator (rows 32 rt ..) in this half.
+__device__ __forceinline__ int elem_row(int v, int half) {
+  return 16 * (v >> 3) + 8 * half + (v & 7);
+}
+
+// The other half's value (lane ^ 32).
+__device__ __forceinline__ float other_half(float x) {
+  return __shfl_xor(x, 32, 64);
+}
+
+}  // namespace attn
+}  // namespace qn

@@ -354,6 +354,9 @@ __device__ __forceinline__ float bf16_hi_to_f32(uint32_t v) {
 __device__ __forceinline__ float bf16_to_f32(uint16_t v) {
   return __builtin_bit_cast(float, ((uint32_t)v) << 16);
 }
+// The float in a word.  (By value: __builtin_bit_cast of an element of a
+// vector reads element 0.)
+__device__ __forceinline__ float word_to_f32(uint32_t v) { return __builtin_bit_cast(float, v); }
 __device__ __forceinline__ uint16_t f32_to_bf16(float x) {
   return (uint16_t)(pack_bf16x2(x, 0.0f) & 0xffffu);
 }

@@ -110,6 +110,83 @@ hipError_t launch_lq_init(const LqArgs& a, hipStream_t stream);
 hipError_t launch_lq_residual(const float* W, const float* L1, const float* L2t, int64_t N,
                               int64_t K, int r, float* R, hipStream_t stream);
 
+// ---- norm.hip: layer norm and root-mean-square norm ----
+constexpr int kNormBF16 = 0, kNormF32 = 1;  // element types (of clip.hip too)
+struct NormArgs {
+  const void* x;      // [rows, width]
+  int64_t rows, width;
+  int x_type;
+  const void* w;      // [width]
+  const void* b;      // [width] or null
+  int w_type;
+  float eps;
+  bool rms;
+  void* y;            // [rows, width], x's type
+  float* mean;        // [rows] (not touched if rms)
+  float* rstd;        // [rows]
+};
+struct NormBwdArgs {
+  const void* dy;
+  const void* x;
+  int64_t rows, width;
+  int x_type;
+  const void* w;
+  int w_type;
+  bool rms;
+  const float* mean;  // unused if rms
+  const float* rstd;
+  void* dx;           // or null
+  void* dw;           // [width], w's type, or null
+  void* db;           // or null
+  float* part;        // norm_bwd_groups rows of width floats, for dw and for db
+};
+int64_t norm_max_width(int type);
+// Workgroups of the backward pass, i.e. rows of partial parameter sums.
+int norm_bwd_groups(int64_t rows, int64_t width, int type);
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
+
+// ---- clip.hip: global gradient norm and clipping ----
+constexpr int kClipNormTable = 240;   // tensors per launch of the sum of squares
+constexpr int kClipScaleTable = 160;  // tensors per launch of the scaling
+constexpr int kClipGrid = 1024;       // workgroups (and partial sums) per launch at most
+struct ClipArgs {
+  int64_t n;
+  const void* const* grads;  // host array of device pointers
+  const int64_t* sizes;      // host
+  const int32_t* types;      // host: kNormBF16 / kNormF32
+  void* const* out;          // host array, or null: in place
+  bool scale;                // false: the norm only
+  float max_norm;
+  float* norm;               // device, 1 float
+  double* part;              // kClipGrid slots per launch of the sum of squares
+};
+hipError_t launch_clip(const ClipArgs& a, hipStream_t stream);
+
+// ---- attention_fwd.hip, attention_bwd.hip ----
+// A [batch, token, head, dim] tensor: element strides (the last one is 1).
+struct AttnView {
+  uint16_t* p;
+  int64_t sb, st, sh;
+};
+struct AttnArgs {
+  AttnView q, k, v, o;         // o: output of the forward, input of the backward pass
+  AttnView dout, dq, dk, dv;   // backward
+  float* lse;                  // [B, H, Sq] dense, [H, Tq] packed
+  float* delta;                // workspace of the backward pass, as lse
+  // packed: sequence s has the query rows cu_q[s] .. cu_q[s + 1] - 1 and the
+  // key rows cu_k[s] .. cu_k[s + 1] - 1 (device, int32); null if dense
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int nseq;                    // sequences (dense: the batch)
+  int64_t Sq, Sk;              // rows: per sequence if dense, in all if packed
+  int H, Hkv, D;
+  float scale;
+  bool causal;
+};
+hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t stream);
+
 // ---- stream.hip: read-only HBM stream (measurement helper) ----
 // Reads bytes / 16 16-byte words of src with `grid` workgroups of 256
 // lanes; writes one word per workgroup to sink[0 .. grid - 1].

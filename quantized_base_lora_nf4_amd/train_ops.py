@@ -1,0 +1,443 @@
+"""Thin torch binding of the operators around the layer: attention, layer and
+root-mean-square norms, and the clipping of gradients by their global norm.
+
+As in :mod:`quantized_base_lora_nf4_amd.ops`: argument checks and marshalling
+only, every call enqueues on ``torch.cuda.current_stream()`` of the tensors'
+device unless a stream is passed, buffers allocated here are allocated on
+that stream, and all arithmetic happens in the HIP kernels.
+"""
+
+import array
+import contextlib
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Heads, check, lib
+from .ops import _stream_obj
+
+_SIXTEEN = (torch.bfloat16, torch.int16, torch.uint16)
+_TYPES = {torch.bfloat16: QLORA_TYPE_BF16, torch.float32: QLORA_TYPE_FP32}
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device, stream):
+    """(stream handle, context to allocate and launch in) for tensors on
+    `device`: the given stream, or the device's current one."""
+    other = device.index is not None and device.index != torch.cuda.current_device()
+    if stream is None:
+        return (torch.cuda.current_stream(device).cuda_stream,
+                torch.cuda.device(device) if other else _HERE)
+    st = _stream_obj(stream)
+    return st.cuda_stream, torch.cuda.stream(st)
+
+
+def _device_of(name: str, t: torch.Tensor) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a GPU")
+    return t.device
+
+
+def _same(name: str, t, shape, dtypes, device) -> None:
+    """Shape, dtype, device and layout of one contiguous tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _bytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _scratch(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    if ws is not None:
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError("ws must be a contiguous tensor on the operands' GPU")
+        if _bytes(ws) >= nbytes:
+            return ws
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+
+def _heads(name: str, t: torch.Tensor, shape, device, packed: bool) -> Heads:
+    """One [batch, row, head, dim] (packed: [row, head, dim]) tensor of any
+    strides that the kernels take."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in _SIXTEEN:
+        raise TypeError(f"{name} must be bf16 (or its 16-bit view), got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st = t.stride()
+    if t.numel() == 0:
+        return Heads(None, 0, 0, 0)
+    # the stride of a dimension of size 1 says nothing
+    st = [0 if n == 1 else s for n, s in zip(shape, st[:-1])] + [st[-1]]
+    if (st[-1] != 1 and shape[-1] != 1) or any(s % 8 for s in st[:-1]):
+        raise ValueError(f"{name} needs contiguous head vectors and strides of a multiple of 8, "
+                         f"has {tuple(t.stride())}")
+    if packed:
+        return Heads(t.data_ptr(), 0, st[0], st[1])
+    return Heads(t.data_ptr(), st[0], st[1], st[2])
+
+
+class _AttnCall:
+    """Checked shapes of an attention call."""
+
+    def __init__(self, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
+        dev = _device_of("q", q)
+        self.packed = cu_seqlens is not None
+        if not self.packed and cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        nd = 3 if self.packed else 4
+        for name, t in (("q", q), ("k", k)):
+            if not isinstance(t, torch.Tensor) or t.dim() != nd:
+                raise ValueError(f"{name} must have {nd} dimensions "
+                                 f"({'[row, head, dim]' if self.packed else '[batch, row, head, dim]'})")
+        h, d = q.shape[-2:]
+        hk = k.shape[-2]
+        if h < 1 or hk < 1 or h % hk:
+            raise ValueError(f"{h} query heads cannot share {hk} key/value heads")
+        self.dev = dev
+        self.q_shape = tuple(q.shape)
+        self.k_shape = ((k.shape[0],) if self.packed else (q.shape[0], k.shape[1])) + (hk, d)
+        cq = ck = None
+        if self.packed:
+            if cu_seqlens_k is None:
+                cu_seqlens_k = cu_seqlens
+                if k.shape[0] != q.shape[0]:
+                    raise ValueError("q and k have different rows: cu_seqlens_k is needed")
+            for name, c in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_seqlens_k)):
+                if not isinstance(c, torch.Tensor) or c.dim() != 1 or c.numel() < 1:
+                    raise ValueError(f"{name} must be a 1-D tensor of offsets")
+                _same(name, c, cu_seqlens.shape, (torch.int32,), dev)
+            cq, ck = cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr()
+            n = cu_seqlens.numel() - 1
+            self.lse_shape = (h, q.shape[0])
+        else:
+            n = q.shape[0]
+            self.lse_shape = (n, h, q.shape[1])
+        if scale is None:
+            scale = 1.0 / math.sqrt(d) if d else 1.0
+        self.c = Attention(n, self.q_shape[-3], self.k_shape[-3], cq, ck, h, hk, d, int(causal),
+                           float(scale))
+        self.q, self.k, self.v = self.heads("q", q), self.heads("k", k), self.heads("v", v)
+
+    def heads(self, name, t):
+        shape = self.k_shape if name in ("k", "v", "dk", "dv") else self.q_shape
+        return _heads(name, t, shape, self.dev, self.packed)
+
+
+def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True,
+                  scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                  cu_seqlens_k: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, stream=None):
+    """softmax(scale q k^T) v per head, and the rows' log-sum-exp (fp32).
+
+    Dense: q [B, Sq, H, D], k and v [B, Sk, Hkv, D]; returns out like q and
+    lse [B, H, Sq].  Packed: q [T, H, D], k and v [Tk, Hkv, D] with the
+    sequences' offsets as an int32 device tensor `cu_seqlens` (and
+    `cu_seqlens_k` if the keys have their own); lse [H, T].  bf16; H a
+    multiple of Hkv; D a multiple of 8 up to 128; views with strides of a
+    multiple of 8 are taken as they are.  Causal: the last query of a sequence
+    sees its last key.  A query that sees no key gets 0 and an lse of -inf.
+    scale defaults to 1 / sqrt(D)."""
+    c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+    st, ctx = _on(c.dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(c.q_shape, dtype=torch.bfloat16, device=c.dev)
+        lse = torch.empty(c.lse_shape, dtype=torch.float32, device=c.dev)
+        check(lib().qlora_attention_fwd(c.c, c.q, c.k, c.v, c.heads("out", out), lse.data_ptr(),
+                                        st), "qlora_attention_fwd")
+    return out, lse
+
+
+def attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                  lse: torch.Tensor, do: torch.Tensor, causal: bool = True,
+                  scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                  cu_seqlens_k: Optional[torch.Tensor] = None, out: Optional[tuple] = None,
+                  ws: Optional[torch.Tensor] = None, stream=None):
+    """(dq, dk, dv) for the output gradient `do`, with o and lse as
+    attention_fwd returned them; the other arguments as there.  `out`: the
+    three tensors to write."""
+    c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+    _same("lse", lse, c.lse_shape, (torch.float32,), c.dev)
+    oh, gh = c.heads("o", o), c.heads("do", do)
+    st, ctx = _on(c.dev, stream)
+    with ctx:
+        if out is None:
+            out = (torch.empty(c.q_shape, dtype=torch.bfloat16, device=c.dev),
+                   torch.empty(c.k_shape, dtype=torch.bfloat16, device=c.dev),
+                   torch.empty(c.k_shape, dtype=torch.bfloat16, device=c.dev))
+        dq, dk, dv = out
+        L = lib()
+        ws = _scratch(int(L.qlora_attention_bwd_workspace_size(c.c)), c.dev, ws)
+        check(L.qlora_attention_bwd(c.c, c.q, c.k, c.v, oh, lse.data_ptr(), gh,
+                                    c.heads("dq", dq), c.heads("dk", dk), c.heads("dv", dv),
+                                    ws.data_ptr(), _bytes(ws), st), "qlora_attention_bwd")
+    return dq, dk, dv
+
+
+def _takeable(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy if its strides are not ones the kernels take."""
+    st = t.stride()
+    ok = st[-1] == 1 and all(s % 8 == 0 for s in st[:-1]) and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+class _AttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
+        o, lse = attention_fwd(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
+        ctx.how = causal, scale
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, cu_seqlens, cu_seqlens_k = ctx.saved_tensors
+        grads = attention_bwd(q, k, v, o, lse, _takeable(do), *ctx.how, cu_seqlens, cu_seqlens_k)
+        return (*grads, None, None, None, None)
+
+
+def attention(q, k, v, causal: bool = True, scale: Optional[float] = None, cu_seqlens=None,
+              cu_seqlens_k=None) -> torch.Tensor:
+    """attention_fwd with gradients for q, k and v (torch autograd); returns
+    the output only."""
+    return _AttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+
+
+# ---------------------------------------------------------------------------
+# Norms
+# ---------------------------------------------------------------------------
+
+def _check_norm(x, weight, others):
+    dev = _device_of("x", x)
+    if x.dim() < 1:
+        raise ValueError("x must have at least 1 dimension")
+    if x.dtype not in _TYPES:
+        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    width = x.shape[-1]
+    _same("weight", weight, (width,), tuple(_TYPES), dev)
+    for name, t, shape, dtype in others:
+        if t is not None:
+            _same(name, t, shape, (dtype,), dev)
+    return dev, x.numel() // width if width else 0, width
+
+
+def norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+             eps: float = 1e-5, rms: bool = False, out: Optional[torch.Tensor] = None,
+             stream=None):
+    """Layer norm (or, with `rms`, root-mean-square norm) over the last
+    dimension of x: y = (x - mean) rstd weight + bias.
+
+    x and y are bfloat16 or float32, weight and bias either (of one type);
+    mean and rstd are float32, one per row, and mean is None with `rms`.
+    Returns (y, mean, rstd)."""
+    dev, rows, width = _check_norm(x, weight, (
+        ("bias", bias, weight.shape, weight.dtype), ("out", out, x.shape, x.dtype)))
+    st, ctx = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty_like(x)
+        mean = None if rms else torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        check(lib().qlora_norm_fwd(x.data_ptr(), rows, width, _TYPES[x.dtype], weight.data_ptr(),
+                                   None if bias is None else bias.data_ptr(),
+                                   _TYPES[weight.dtype], float(eps), int(rms), out.data_ptr(),
+                                   None if rms else mean.data_ptr(), rstd.data_ptr(), st),
+              "qlora_norm_fwd")
+    return out, mean, rstd
+
+
+def norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+             mean: Optional[torch.Tensor], rstd: torch.Tensor, rms: bool = False,
+             need_dx: bool = True, need_dw: bool = True, need_db: Optional[bool] = None,
+             ws: Optional[torch.Tensor] = None, stream=None):
+    """(dx, dweight, dbias) of norm_fwd for the output gradient dy, from its
+    mean and rstd.  dbias is computed without `rms` unless need_db says
+    otherwise; what is not computed is None."""
+    dev, rows, width = _check_norm(x, weight, (
+        ("dy", dy, x.shape, x.dtype), ("rstd", rstd, x.shape[:-1], torch.float32),
+        ("mean", None if rms else mean, x.shape[:-1], torch.float32)))
+    if dy is None or rstd is None or (mean is None and not rms):
+        raise ValueError("dy, rstd and (without rms) mean are needed")
+    if need_db is None:
+        need_db = not rms
+    st, ctx = _on(dev, stream)
+    with ctx:
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(weight) if need_dw else None
+        db = torch.empty_like(weight) if need_db else None
+        L = lib()
+        need = int(L.qlora_norm_bwd_workspace_size(rows, width, _TYPES[x.dtype]))
+        ws = _scratch(need, dev, ws)
+        check(L.qlora_norm_bwd(dy.data_ptr(), x.data_ptr(), rows, width, _TYPES[x.dtype],
+                               weight.data_ptr(), _TYPES[weight.dtype], int(rms),
+                               None if rms else mean.data_ptr(), rstd.data_ptr(),
+                               *(None if t is None else t.data_ptr() for t in (dx, dw, db)),
+                               ws.data_ptr(), _bytes(ws), st), "qlora_norm_bwd")
+    return dx, dw, db
+
+
+class _NormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, rms):
+        x = x.contiguous()
+        y, mean, rstd = norm_fwd(x, weight, bias, eps, rms)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.rms = rms
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grads = norm_bwd(dy.contiguous(), x, weight, mean, rstd, ctx.rms, need_dx=need[0],
+                         need_dw=need[1], need_db=need[2])
+        return (*grads, None, None)
+
+
+def norm(x, weight, bias=None, eps: float = 1e-5, rms: bool = False) -> torch.Tensor:
+    """norm_fwd with gradients for x, weight and bias (torch autograd);
+    returns y only."""
+    return _NormFunction.apply(x, weight, bias, eps, rms)
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm over the last dimension, with weight and bias."""
+
+    def __init__(self, width: int, eps: float = 1e-5, device="cuda", dtype=torch.float32):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(width, device=device, dtype=dtype))
+        self.bias = torch.nn.Parameter(torch.zeros(width, device=device, dtype=dtype))
+
+    def forward(self, x):
+        return norm(x, self.weight, self.bias, self.eps)
+
+
+class RMSNorm(torch.nn.Module):
+    """Root-mean-square norm over the last dimension, with a weight."""
+
+    def __init__(self, width: int, eps: float = 1e-5, device="cuda", dtype=torch.float32):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(width, device=device, dtype=dtype))
+
+    def forward(self, x):
+        return norm(x, self.weight, None, self.eps, rms=True)
+
+
+# ---------------------------------------------------------------------------
+# Gradient norm and clipping
+# ---------------------------------------------------------------------------
+
+def _addresses(values) -> "array.array":
+    return array.array("Q", values)
+
+
+def _grad_arrays(name: str, grads):
+    """(device, sizes, types) of a list of gradients, after one look at each."""
+    dev = _device_of(f"{name}[0]", grads[0])
+    kinds = {(t.dtype, t.device, t.is_contiguous()) for t in grads}
+    for dt, d, contiguous in kinds:
+        if dt not in _TYPES:
+            raise TypeError(f"{name} must be bfloat16 or float32, one is {dt}")
+        if d != dev:
+            raise ValueError(f"{name} are on {dev} and {d}, expected one GPU")
+        if not contiguous:
+            raise ValueError(f"{name} must be contiguous")
+    if len({k[0] for k in kinds}) == 1:
+        types = array.array("i", [_TYPES[grads[0].dtype]]) * len(grads)
+    else:
+        types = array.array("i", [_TYPES[t.dtype] for t in grads])
+    return dev, [t.numel() for t in grads], types
+
+
+def _ptr_of(a: "array.array") -> int:
+    return a.buffer_info()[0]
+
+
+def _clip_call(grads, max_norm, out, ws, stream):
+    grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+    for g in grads:
+        if not isinstance(g, torch.Tensor):
+            raise TypeError("gradients must be torch tensors")
+    if max_norm is not None and not float(max_norm) >= 0.0:
+        raise ValueError(f"max_norm must be at least 0, got {max_norm}")
+    if not grads:
+        raise ValueError("there are no gradients")
+    dev, sizes, types = _grad_arrays("gradients", grads)
+    ptrs = _addresses([g.data_ptr() for g in grads])
+    outs = None
+    if isinstance(out, torch.Tensor):
+        if out.dtype != grads[0].dtype or any(t != types[0] for t in types):
+            raise TypeError("a flat out takes gradients of its own dtype only")
+        _same("out", out, (sum(sizes),), (grads[0].dtype,), dev)
+        at, step, each = out.data_ptr(), out.element_size(), []
+        for n in sizes:
+            each.append(at)
+            at += n * step
+        outs = _addresses(each)
+    elif out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out has {len(out)} tensors for {len(grads)} gradients")
+        for g, o in zip(grads, out):
+            _same("out", o, g.shape, (g.dtype,), dev)
+        outs = _addresses([o.data_ptr() for o in out])
+    nbytes = array.array("q", sizes)
+    n = len(grads)
+    st, ctx = _on(dev, stream)
+    with ctx:
+        norm_out = torch.empty(1, dtype=torch.float32, device=dev)
+        L = lib()
+        ws = _scratch(int(L.qlora_clip_workspace_size(n)), dev, ws)
+        if max_norm is None:
+            check(L.qlora_grad_norm(n, _ptr_of(ptrs), _ptr_of(nbytes), _ptr_of(types),
+                                    norm_out.data_ptr(), ws.data_ptr(), _bytes(ws), st),
+                  "qlora_grad_norm")
+        else:
+            check(L.qlora_clip_grad_norm(n, _ptr_of(ptrs), _ptr_of(nbytes), _ptr_of(types),
+                                         float(max_norm), None if outs is None else _ptr_of(outs),
+                                         norm_out.data_ptr(), ws.data_ptr(), _bytes(ws), st),
+                  "qlora_clip_grad_norm")
+    return norm_out
+
+
+def grad_norm(grads, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The 2-norm of all gradients together (a one-element float32 device
+    tensor, written on the stream).  grads: contiguous bfloat16 or float32
+    tensors, in any mixture; None entries are left out."""
+    return _clip_call(grads, None, None, ws, stream)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Scale the gradients by min(1, max_norm / (norm + 1e-6)) and return
+    their norm before that (a one-element float32 device tensor).
+
+    out: None scales in place; a list of tensors (one per gradient that is
+    not None, same shape and dtype) takes the scaled gradients instead, and
+    so does one flat tensor of their dtype, one gradient after the other."""
+    return _clip_call(grads, float(max_norm), out, ws, stream)
