@@ -50,13 +50,26 @@ struct Work {
   bool valid;
 };
 
+// The order of the work: workgroup id -> (head of the batch, slot).
 // Workgroups go to the 8 XCDs round-robin by id, and each XCD has its own
-// L2: a contiguous range of work per XCD keeps the tiles of one head, and the
-// heads that share K and V, on one L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t p, int64_t total) {
-  const int64_t per = total >> 3;
-  if (p >= per * 8) return p;
-  return (p & 7) * per + (p >> 3);
+// L2: an XCD gets a contiguous range of heads, so that those that share K
+// and V share an L2.  Within its range the slots are the outer index: the
+// slots that take longest come first for all heads, and the last workgroups
+// to start are short ones.
+struct Place {
+  int64_t head, slot;
+};
+__device__ __forceinline__ Place place_of(int64_t id, int64_t heads, int64_t slots) {
+  Place p;
+  if (heads % 8 == 0) {
+    const int64_t per = heads >> 3, j = id >> 3;
+    p.head = (id & 7) * per + j % per;
+    p.slot = j / per;
+  } else {
+    p.head = id % heads;
+    p.slot = id / heads;
+  }
+  return p;
 }
 
 __device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
@@ -72,13 +85,13 @@ __device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
 // ones give wrong results but no access out of range.
 // kKeys: the columns are keys (the dK/dV kernel), else queries.
 template <bool kKeys>
-__device__ __forceinline__ Work find_work(const AttnArgs& p, int64_t id, int64_t slots,
-                                          int heads) {
+__device__ __forceinline__ Work find_work(const AttnArgs& p, int64_t slots, int heads) {
   Work w;
-  w.head = (int)((id / slots) % heads);
-  const int64_t slot = id % slots;
+  const Place at = place_of(blockIdx.x, gridDim.x / slots, slots);
+  w.head = (int)(at.head % heads);
+  const int64_t slot = at.slot;
   if (!p.cu_q) {
-    w.batch = id / slots / heads;
+    w.batch = at.head / heads;
     w.q0 = w.k0 = 0;
     w.lq = (int)p.Sq;
     w.lk = (int)p.Sk;
@@ -136,6 +149,18 @@ inline int64_t tile_slots(const AttnArgs& a, int64_t cols) {
 
 // ---- tiles in LDS ----
 
+// v, in a form the compiler cannot compute from ahead: what is derived from
+// it would otherwise be kept in registers across the loop over the tiles.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// A wave-uniform float in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+
 template <int DP>
 struct Geo {
   static constexpr int kChunks = DP / 8;           // 16-byte chunks per row
@@ -155,47 +180,58 @@ __device__ __forceinline__ int chunk_mask(int row) {
 
 typedef __attribute__((address_space(3))) uint16_t lds_u16;
 
-// The per-lane byte offsets of this wave's loads of a tile: load i fills
-// 1024 consecutive bytes of LDS (64 / kChunks rows), lane l's 16 bytes at
-// 16 l, so the lane fetches the chunk that the mask puts there.  Rows past
+// This wave's loads of a tile: load i fills 1024 consecutive bytes of LDS
+// (kRows rows) at row (i kWaves + wave) kRows, lane l's 16 bytes at 16 l, so the
+// lane fetches the chunk that the mask puts there: the same one in every load,
+// since the loads' rows agree in the bits that the mask looks at.  Rows past
 // the last one read the last row again, chunks past D the row's first.
-template <int DP>
 struct TileLoader {
-  int row[Geo<DP>::kLoads];   // tile row
-  int cols[Geo<DP>::kLoads];  // byte offset within the row
+  int row, col;  // row of load 0; byte offset within the row
 };
 
 template <int DP>
-__device__ __forceinline__ void tile_loader(TileLoader<DP>& t, int D, int wave, int lane) {
+__device__ __forceinline__ TileLoader tile_loader(int D, int wave, int lane) {
   constexpr int C = Geo<DP>::kChunks, R = 64 / C;
+  static_assert((kWaves * R) % 16 == 0, "the mask looks at four bits of the row");
+  TileLoader t;
+  t.row = wave * R + lane / C;
+  const int c = (lane % C) ^ chunk_mask<DP>(t.row);
+  t.col = c * 8 < D ? c * 16 : 0;
+  return t;
+}
+
+// Issues the loads of 64 rows at `base` (row stride st elements), of which
+// `left` (at least 1) exist, into the tile at `lds`.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint16_t* lds, const TileLoader& t, const uint16_t* base,
+                                          int64_t st, int left, int wave) {
+  constexpr int R = kWaves * 64 / Geo<DP>::kChunks;  // rows from one load to the next
+  const int st2 = (int)(st * 2);
+  // 64 rows of at most 2^22 elements: below 2^31 bytes
+  const __amdgpu_buffer_rsrc_t rsrc = bytes_rsrc(base, 0x7fffffff);
+  if (left >= kTile) {
+    const int voff = t.row * st2 + t.col;
 #pragma unroll
-  for (int i = 0; i < Geo<DP>::kLoads; ++i) {
-    const int r = (i * kWaves + wave) * R + lane / C;
-    const int c = (lane % C) ^ chunk_mask<DP>(r);
-    t.row[i] = r;
-    t.cols[i] = c * 8 < D ? c * 16 : 0;
+    for (int i = 0; i < Geo<DP>::kLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(lds + (i * kWaves + wave) * 512), 16,
+          voff, i * R * st2, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Geo<DP>::kLoads; ++i) {
+      int row = opaque(t.row) + i * R;
+      if (row >= left) row = left - 1;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(lds + (i * kWaves + wave) * 512), 16,
+          row * st2 + t.col, 0, 0, 0);
+    }
   }
 }
 
-// Issues the loads of rows row0 .. row0 + 63 (clamped to nrows - 1) of the
-// matrix at base (row stride st elements) into the tile at `lds`.
-template <int DP>
-__device__ __forceinline__ void load_tile(uint16_t* lds, const TileLoader<DP>& t,
-                                          const uint16_t* base, int64_t st, int row0, int nrows,
-                                          int wave) {
-  const int left = nrows - row0;  // >= 1
-  const int64_t bytes = ((int64_t)((left < kTile ? left : kTile) - 1) * st + DP) * 2;
-  const __amdgpu_buffer_rsrc_t rsrc =
-      bytes_rsrc(base + (int64_t)row0 * st, bytes < 0x7fffffff ? bytes : 0x7fffffff);
-#pragma unroll
-  for (int i = 0; i < Geo<DP>::kLoads; ++i) {
-    const int r = t.row[i] < left ? t.row[i] : left - 1;
-    const int voff = r * (int)(st * 2) + t.cols[i];
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rsrc, (__attribute__((address_space(3))) void*)(lds + (i * kWaves + wave) * 512), 16, voff,
-        0, 0, 0);
-  }
-}
+// Nothing is scheduled across this point.  The products read their LDS
+// operands a fixed number of steps ahead; left to itself the compiler moves
+// all reads of a tile to its front and runs out of registers.
+__device__ __forceinline__ void step_fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // This wave's tile loads have landed, and every wave is here.
 __device__ __forceinline__ void tiles_ready() {
@@ -211,9 +247,9 @@ __device__ __forceinline__ int swap23(int r) {
   return (r & ~12) | ((r & 4) << 1) | ((r & 8) >> 1);
 }
 
-// A lane's offset (elements) of its fragments within a tile.  The dimension
-// steps only change bits of the chunk index that nothing else adds to, so
-// they are exclusive-ored into one base per kind of read.
+// A lane's byte offset of its fragments within a tile.  The dimension steps
+// only change bits of the chunk index that nothing else adds to, so they are
+// exclusive-ored into one base per kind of read.
 struct FragOff {
   int row;  // rows as A rows
   int tr;   // transposed
@@ -228,32 +264,35 @@ template <int DP>
 __device__ __forceinline__ FragOff frag_off(int lane) {
   FragOff f;
   const int r = swap23(lane & 31);
-  f.row = r * DP + (((lane >> 5) ^ chunk_mask<DP>(r)) << 3);
+  f.row = r * DP * 2 + (((lane >> 5) ^ chunk_mask<DP>(r)) << 4);
   const int g = lane >> 4, j = lane & 15;
   const int x = 4 * (g & 1) + (j & 3);                       // which 4 A rows
   const int x4 = (x & 4) | ((x & 1) << 1) | ((x >> 1) & 1);  // the 4 dimensions they stand for
   const int rt = 8 * (g >> 1) + (j >> 2);
-  f.tr = rt * DP + (((x4 >> 1) ^ chunk_mask<DP>(rt)) << 3) + 4 * (x4 & 1);
+  f.tr = rt * DP * 2 + (((x4 >> 1) ^ chunk_mask<DP>(rt)) << 4) + 8 * (x4 & 1);
   return f;
 }
 
-// Tile rows 32 rt + swap23(lane % 32), dimensions 16 s + 8 (lane / 32) + 0..7.
+// Tile rows 32 rt + swap23(lane % 32), dimensions 16 s + 8 (lane / 32) + 0..7,
+// from the offset `row`.
 template <int DP>
-__device__ __forceinline__ bf16x8 read_rows(const uint16_t* tile, const FragOff& f, int s, int rt) {
-  return *reinterpret_cast<const bf16x8*>(tile + (f.row ^ (s << 4)) + rt * 32 * DP);
+__device__ __forceinline__ bf16x8 read_rows(const uint16_t* tile, int row, int s, int rt) {
+  return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(tile) + (row ^ (s << 5)) +
+                                          rt * 64 * DP);
 }
 
-// Tile rows 16 slab + 8 (lane / 32) + 0..7 of dimension 32 d + swap23(lane % 32).
+// Tile rows 16 slab + 8 (lane / 32) + 0..7 of dimension 32 d + swap23(lane % 32),
+// from the offset `tr`.
 template <int DP>
-__device__ __forceinline__ bf16x8 read_tr(const uint16_t* tile, const FragOff& f, int d, int slab) {
+__device__ __forceinline__ bf16x8 read_tr(const uint16_t* tile, int tr, int d, int slab) {
   typedef short v4i16 __attribute__((ext_vector_type(4)));
   typedef short v8i16 __attribute__((ext_vector_type(8)));
   typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-  const int o = f.tr ^ (d << 5);
+  const char* t = reinterpret_cast<const char*>(tile) + slab * 32 * DP;
+  const int o = tr ^ (d << 6);
   // the row 4 further on has the lowest bit of its chunk mask flipped
-  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(tile + o + slab * 16 * DP));
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_v4i16*)(tile + (o ^ 8) + slab * 16 * DP + 4 * DP));
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + o));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + (o ^ 16) + 8 * DP));
   const v8i16 v = v8i16{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8, v);
 }
@@ -266,8 +305,9 @@ __device__ __forceinline__ void load_cols(bf16x8 (&f)[Geo<DP>::kSteps], const ui
 #pragma unroll
   for (int s = 0; s < Geo<DP>::kSteps; ++s) {
     const int d = 16 * s + 8 * (lane >> 5);
-    const u32x4 z = {0u, 0u, 0u, 0u};
-    f[s] = as_bf16x8(d < D ? *reinterpret_cast<const u32x4*>(row + d) : z);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(row + (d < D ? d : 0));
+    const uint32_t keep = d < D ? 0xffffffffu : 0u;
+    f[s] = as_bf16x8(u32x4{v[0] & keep, v[1] & keep, v[2] & keep, v[3] & keep});
   }
 }
 

@@ -35,40 +35,96 @@ struct DqState {
   float c, lse, delta;  // scale log2(e); lse in powers of two, +inf if the row sees no key
 };
 
-// One tile of keys; this lane's query sees tile rows 0 .. last.
-template <int DP, bool kMask>
+// acc_x += rows of tile x times xb, acc_y likewise, 32 tile rows from 32 rt on;
+// operands are read kAhead steps before their use.
+template <int DP, int kAhead>
+__device__ __forceinline__ void scores(f32x16& acc_x, f32x16& acc_y, const uint16_t* tx,
+                                       const uint16_t* ty, const bf16x8 (&xb)[Geo<DP>::kSteps],
+                                       const bf16x8 (&yb)[Geo<DP>::kSteps], const FragOff& f,
+                                       int rt) {
+  constexpr int N = Geo<DP>::kSteps;
+  const int row = opaque(f.row);
+  bf16x8 x[N], y[N];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    x[i] = read_rows<DP>(tx, row, i, rt);
+    y[i] = read_rows<DP>(ty, row, i, rt);
+  }
+  step_fence();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + kAhead < N) {
+      x[i + kAhead] = read_rows<DP>(tx, row, i + kAhead, rt);
+      y[i + kAhead] = read_rows<DP>(ty, row, i + kAhead, rt);
+    }
+    acc_x = mfma32(x[i], xb[i], acc_x);
+    acc_y = mfma32(y[i], yb[i], acc_y);
+    step_fence();
+  }
+}
+
+// Tile rows 32 rt .. times xb; operands are read two steps before their use.
+template <int DP>
+__device__ __forceinline__ f32x16 rows_times(const uint16_t* tile,
+                                             const bf16x8 (&xb)[Geo<DP>::kSteps], const FragOff& f,
+                                             int rt) {
+  constexpr int N = Geo<DP>::kSteps, kAhead = 2;
+  const int row = opaque(f.row);
+  f32x16 acc = f32x16{};
+  bf16x8 x[N];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = read_rows<DP>(tile, row, i, rt);
+  step_fence();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + kAhead < N) x[i + kAhead] = read_rows<DP>(tile, row, i + kAhead, rt);
+    acc = mfma32(x[i], xb[i], acc);
+    step_fence();
+  }
+  return acc;
+}
+
+// One tile of keys; this lane's query sees tile rows 0 .. last (mask: not
+// all of them in some lane).
+template <int DP>
 __device__ __forceinline__ void dq_tile(DqState<DP>& st, const uint16_t* kt, const uint16_t* vt,
-                                        const FragOff& f, int last, int half) {
+                                        const FragOff& f, bool mask, int last, int half) {
+  constexpr int T = Geo<DP>::kDT, kAhead = 2;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
+    const int tr = opaque(f.tr);
     f32x16 s = f32x16{}, dp = f32x16{};
+    scores<DP, kAhead>(s, dp, kt, vt, st.q, st.g, f, r);
+    bf16x8 x[2 * T];
 #pragma unroll
-    for (int i = 0; i < Geo<DP>::kSteps; ++i) {
-      s = mfma32(read_rows<DP>(kt, f, i, r), st.q[i], s);
-      dp = mfma32(read_rows<DP>(vt, f, i, r), st.g[i], dp);
+    for (int j = 0; j < kAhead; ++j) x[j] = read_tr<DP>(kt, tr, j % T, 2 * r + j / T);
+    if (mask) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        if (32 * r + elem_row(v, half) > last) s[v] = -kInf;
     }
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      if (kMask && 32 * r + elem_row(v, half) > last) s[v] = -kInf;
+    for (int v = 0; v < 16; ++v)
       s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], st.c, -st.lse)) * (dp[v] - st.delta);
-    }
+    const bf16x8 ds[2] = {pack8(s, 0), pack8(s, 1)};
+    step_fence();
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const bf16x8 ds = pack8(s, b);
-#pragma unroll
-      for (int t = 0; t < Geo<DP>::kDT; ++t)
-        st.dq[t] = mfma32(read_tr<DP>(kt, f, t, 2 * r + b), ds, st.dq[t]);
+    for (int j = 0; j < 2 * T; ++j) {
+      if (j + kAhead < 2 * T)
+        x[j + kAhead] = read_tr<DP>(kt, tr, (j + kAhead) % T, 2 * r + (j + kAhead) / T);
+      st.dq[j % T] = mfma32(x[j], ds[j / T], st.dq[j % T]);
+      step_fence();
     }
   }
 }
 
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64, 1) void k_attn_bwd_dq(AttnArgs p, int64_t slots) {
+__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dq(AttnArgs p, int64_t slots) {
   __shared__ __attribute__((aligned(16))) uint16_t k0[Geo<DP>::kElems], v0[Geo<DP>::kElems];
   __shared__ __attribute__((aligned(16))) uint16_t k1[Geo<DP>::kElems], v1[Geo<DP>::kElems];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Work w = find_work<false>(p, xcd_order(blockIdx.x, gridDim.x), slots, p.H);
+  const Work w = find_work<false>(p, slots, p.H);
   if (!w.valid) return;
   const int tile = p.causal ? w.ntiles - 1 - w.tile : w.tile;
   const int col0 = tile * kBlock;
@@ -100,12 +156,11 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_bwd_dq(AttnArgs p, int6
   if (half == 0 && row < w.lq) p.delta[stat] = st.delta;
   const float lse = p.lse[stat];
   st.lse = lse == -kInf ? kInf : lse * kLog2e;
-  st.c = p.scale * kLog2e;
+  st.c = uniform(p.scale * kLog2e);
 #pragma unroll
   for (int t = 0; t < Geo<DP>::kDT; ++t) st.dq[t] = f32x16{};
   const FragOff f = frag_off<DP>(lane);
-  TileLoader<DP> ld;
-  tile_loader<DP>(ld, p.D, wave, lane);
+  const TileLoader ld = tile_loader<DP>(p.D, wave, lane);
 
   int keys = w.lk;
   if (p.causal) {
@@ -122,27 +177,25 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_bwd_dq(AttnArgs p, int6
   auto step = [&](const uint16_t* kt, const uint16_t* vt, int j) {
     const int r0 = j * kTile;
     if (first >= w.lq || r0 > seen_last) return;
-    if (r0 + kTile - 1 <= seen_first && r0 + kTile <= w.lk)
-      dq_tile<DP, false>(st, kt, vt, f, 0, half);
-    else
-      dq_tile<DP, true>(st, kt, vt, f, mine - r0, half);
+    const bool mask = r0 + kTile - 1 > seen_first || r0 + kTile > w.lk;
+    dq_tile<DP>(st, kt, vt, f, mask, mine - r0, half);
   };
   if (nt > 0) {
-    load_tile<DP>(k0, ld, kb, p.k.st, 0, w.lk, wave);
-    load_tile<DP>(v0, ld, vb, p.v.st, 0, w.lk, wave);
+    load_tile<DP>(k0, ld, kb, p.k.st, w.lk, wave);
+    load_tile<DP>(v0, ld, vb, p.v.st, w.lk, wave);
   }
   for (int j = 0; j < nt; j += 2) {
     tiles_ready();
     if (j + 1 < nt) {
-      load_tile<DP>(k1, ld, kb, p.k.st, (j + 1) * kTile, w.lk, wave);
-      load_tile<DP>(v1, ld, vb, p.v.st, (j + 1) * kTile, w.lk, wave);
+      load_tile<DP>(k1, ld, kb + (j + 1) * (kTile * p.k.st), p.k.st, w.lk - (j + 1) * kTile, wave);
+      load_tile<DP>(v1, ld, vb + (j + 1) * (kTile * p.v.st), p.v.st, w.lk - (j + 1) * kTile, wave);
     }
     step(k0, v0, j);
     if (j + 1 >= nt) break;
     tiles_ready();
     if (j + 2 < nt) {
-      load_tile<DP>(k0, ld, kb, p.k.st, (j + 2) * kTile, w.lk, wave);
-      load_tile<DP>(v0, ld, vb, p.v.st, (j + 2) * kTile, w.lk, wave);
+      load_tile<DP>(k0, ld, kb + (j + 2) * (kTile * p.k.st), p.k.st, w.lk - (j + 2) * kTile, wave);
+      load_tile<DP>(v0, ld, vb + (j + 2) * (kTile * p.v.st), p.v.st, w.lk - (j + 2) * kTile, wave);
     }
     step(k1, v1, j + 1);
   }
@@ -158,21 +211,14 @@ template <int DP>
 struct DkvState {
   bf16x8 k[Geo<DP>::kSteps], v[Geo<DP>::kSteps];  // this lane's rows of K and V
   f32x16 dk[Geo<DP>::kDT], dv[Geo<DP>::kDT];
-  float c;
-};
-
-// Row statistics of a tile, spread over the lanes: within each group of 16
-// lanes, lane i holds those of the row that element i of a score accumulator
-// has in this half.
-struct RowStats {
-  float lse[2], delta[2];  // rows 0..31 and 32..63; lse / scale, +inf for a row to leave out
+  float c, inv_scale;
 };
 
 // Lane i's value in every lane of its group of 16.
 template <int I>
 __device__ __forceinline__ float group_lane(float x) {
   return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x150 + I, 0xf, 0xf, false));
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x150 + I, 0xf, 0xf, true));
 }
 
 template <class F, int... I>
@@ -180,49 +226,79 @@ __device__ __forceinline__ void each16(F&& f, std::integer_sequence<int, I...>) 
   (f(std::integral_constant<int, I>{}), ...);
 }
 
-// One tile of queries; this lane's key is seen by tile rows `from` and up.
-template <int DP, bool kMask>
+// One tile of queries; this lane's key is seen by tile rows `from` and up
+// (mask: not by all of them in some lane).
+// stats: lse and D of the tile's 64 rows.  Within each group of 16 lanes, lane
+// i takes those of the row that element i of a score accumulator has in this
+// half, and the elements get them by a lane broadcast within the group.
+template <int DP>
 __device__ __forceinline__ void dkv_tile(DkvState<DP>& st, const uint16_t* qt, const uint16_t* gt,
-                                         const RowStats& rs, const FragOff& f, int from,
-                                         int half) {
+                                         const float* stats, int left, const FragOff& f, bool mask,
+                                         int from, int half, int lane) {
+  constexpr int T = Geo<DP>::kDT;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    f32x16 s = f32x16{}, dp = f32x16{};
+    const int tr = opaque(f.tr);
+    const int i = 32 * r + elem_row(lane & 15, half);
+    float lse = stats[i];
+    const float delta = stats[kTile + i];
+    // rows past the end, and rows that see no key, have no probabilities
+    lse = i < left && lse != -kInf ? lse * st.inv_scale : kInf;
+    f32x16 s = rows_times<DP>(qt, st.k, f, r);
+    if (mask) {
 #pragma unroll
-    for (int i = 0; i < Geo<DP>::kSteps; ++i) {
-      s = mfma32(read_rows<DP>(qt, f, i, r), st.k[i], s);
-      dp = mfma32(read_rows<DP>(gt, f, i, r), st.v[i], dp);
+      for (int v = 0; v < 16; ++v)
+        if (32 * r + elem_row(v, half) < from) s[v] = -kInf;
     }
-    each16(
-        [&](auto vc) {
-          constexpr int v = decltype(vc)::value;
-          float x = (s[v] - group_lane<v>(rs.lse[r])) * st.c;
-          if (kMask && 32 * r + elem_row(v, half) < from) x = -kInf;
-          s[v] = __builtin_amdgcn_exp2f(x);
-          dp[v] = s[v] * (dp[v] - group_lane<v>(rs.delta[r]));
-        },
-        std::make_integer_sequence<int, 16>{});
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const bf16x8 pb = pack8(s, b), ds = pack8(dp, b);
-#pragma unroll
-      for (int t = 0; t < Geo<DP>::kDT; ++t) {
-        st.dv[t] = mfma32(read_tr<DP>(gt, f, t, 2 * r + b), pb, st.dv[t]);
-        st.dk[t] = mfma32(read_tr<DP>(qt, f, t, 2 * r + b), ds, st.dk[t]);
+    each16([&](auto vc) {
+      constexpr int v = decltype(vc)::value;
+      s[v] = __builtin_amdgcn_exp2f((s[v] - group_lane<v>(lse)) * st.c);
+      if (v % 4 == 3) step_fence();
+    }, std::make_integer_sequence<int, 16>{});
+    f32x16 dp = rows_times<DP>(gt, st.v, f, r);
+    bf16x8 x[2 * T], y[2 * T];
+    x[0] = read_tr<DP>(gt, tr, 0, 2 * r);
+    y[0] = read_tr<DP>(qt, tr, 0, 2 * r);
+    u32x4 pw[2], dw[2];  // P and dS as operands
+    each16([&](auto vc) {
+      constexpr int v = decltype(vc)::value;
+      dp[v] = s[v] * (dp[v] - group_lane<v>(delta));
+      if constexpr (v % 2 == 1) {
+        pw[v / 8][v / 2 % 4] = pack_bf16x2(s[v - 1], s[v]);
+        dw[v / 8][v / 2 % 4] = pack_bf16x2(dp[v - 1], dp[v]);
+        step_fence();
       }
+    }, std::make_integer_sequence<int, 16>{});
+    const bf16x8 pb[2] = {as_bf16x8(pw[0]), as_bf16x8(pw[1])};
+    const bf16x8 ds[2] = {as_bf16x8(dw[0]), as_bf16x8(dw[1])};
+    step_fence();
+#pragma unroll
+    for (int j = 0; j < 2 * T; ++j) {
+      if (j + 1 < 2 * T) {
+        x[j + 1] = read_tr<DP>(gt, tr, (j + 1) % T, 2 * r + (j + 1) / T);
+        y[j + 1] = read_tr<DP>(qt, tr, (j + 1) % T, 2 * r + (j + 1) / T);
+      }
+      st.dv[j % T] = mfma32(x[j], pb[j / T], st.dv[j % T]);
+      st.dk[j % T] = mfma32(y[j], ds[j / T], st.dk[j % T]);
+      step_fence();
     }
   }
 }
 
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64, 1) void k_attn_bwd_dkv(AttnArgs p, int64_t slots) {
+__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int64_t slots) {
   __shared__ __attribute__((aligned(16))) uint16_t q0[Geo<DP>::kElems], g0[Geo<DP>::kElems];
   __shared__ __attribute__((aligned(16))) uint16_t q1[Geo<DP>::kElems], g1[Geo<DP>::kElems];
+  __shared__ float s0[2 * kTile], s1[2 * kTile];  // lse, then D, of the tile's rows
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Work w = find_work<true>(p, xcd_order(blockIdx.x, gridDim.x), slots, p.Hkv);
+  const Work w = find_work<true>(p, slots, p.Hkv);
   if (!w.valid) return;
-  const int col0 = w.tile * kBlock;  // causal: the first keys are seen by the most queries
+  // causal: the first keys are seen by the most queries, so they come first;
+  // from the middle on, the last tiles come first.
+  const int mid = (w.ntiles + 1) / 2;
+  const int tile = p.causal && w.tile >= mid ? w.ntiles - 1 - (w.tile - mid) : w.tile;
+  const int col0 = tile * kBlock;
   if (col0 >= w.lk) return;
   const int off = w.lk - w.lq;       // query i sees keys 0 .. i + off
   const int share = p.H / p.Hkv;
@@ -239,11 +315,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_bwd_dkv(AttnArgs p, int
     st.dk[t] = f32x16{};
     st.dv[t] = f32x16{};
   }
-  st.c = p.scale * kLog2e;
-  const float inv_scale = 1.0f / p.scale;
+  st.c = uniform(p.scale * kLog2e);
+  st.inv_scale = uniform(1.0f / p.scale);
   const FragOff f = frag_off<DP>(lane);
-  TileLoader<DP> ld;
-  tile_loader<DP>(ld, p.D, wave, lane);
+  const TileLoader ld = tile_loader<DP>(p.D, wave, lane);
 
   // tiles of queries that see any of the workgroup's keys
   const int ntq = (w.lq + kTile - 1) / kTile;
@@ -251,54 +326,52 @@ __global__ __launch_bounds__(kWaves * 64, 1) void k_attn_bwd_dkv(AttnArgs p, int
   if (p.causal && col0 - off > 0) t0 = (col0 - off) / kTile;
   const int per = ntq > t0 ? ntq - t0 : 0;
   const int nt = per * share;
-  const int stat_row = elem_row(lane & 15, half);
-
-  // Step n: query tile t0 + n % per of head n / per of the group.
-  int ihead = 0, itile = t0;  // of the next step to issue
-  RowStats nrs;
-  auto issue = [&](uint16_t* qb, uint16_t* gb) {
-    const int head = w.head * share + ihead;
-    const int r0 = itile * kTile;
-    load_tile<DP>(qb, ld, p.q.p + w.batch * p.q.sb + w.q0 * p.q.st + head * p.q.sh, p.q.st, r0,
-                  w.lq, wave);
-    load_tile<DP>(gb, ld, p.dout.p + w.batch * p.dout.sb + w.q0 * p.dout.st + head * p.dout.sh,
-                  p.dout.st, r0, w.lq, wave);
-    const int64_t stat = (w.batch * p.H + head) * p.Sq + w.q0;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = r0 + 32 * r + stat_row;
-      const int ic = i < w.lq ? i : w.lq - 1;
-      const float lse = p.lse[stat + ic], delta = p.delta[stat + ic];
-      // rows past the end, and rows that see no key, have no probabilities
-      nrs.lse[r] = i < w.lq && lse != -kInf ? lse * inv_scale : kInf;
-      nrs.delta[r] = delta;
-    }
+  // Step n: query tile t0 + n % per of head n / per of the group.  The
+  // pointers are those of the next step to issue.
+  const int head0 = w.head * share;
+  const int64_t row0 = w.q0 + (int64_t)t0 * kTile;
+  const uint16_t* qp = p.q.p + w.batch * p.q.sb + row0 * p.q.st + head0 * p.q.sh;
+  const uint16_t* gp = p.dout.p + w.batch * p.dout.sb + row0 * p.dout.st + head0 * p.dout.sh;
+  const float* sp = (wave & 1 ? p.delta : p.lse) + (w.batch * p.H + head0) * p.Sq + row0;
+  const int64_t back = (int64_t)per * kTile;  // from the end of a head's rows to their start
+  int itile = t0;
+  auto issue = [&](uint16_t* qb, uint16_t* gb, float* sb) {
+    const int left = w.lq - itile * kTile;
+    load_tile<DP>(qb, ld, qp, p.q.st, left, wave);
+    load_tile<DP>(gb, ld, gp, p.dout.st, left, wave);
+    if (wave < 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          bytes_rsrc(sp, 0x7fffffff),
+          (__attribute__((address_space(3))) void*)(sb + wave * kTile), 4,
+          4 * (lane < left ? lane : left - 1), 0, 0, 0);
+    qp += kTile * p.q.st;
+    gp += kTile * p.dout.st;
+    sp += kTile;
     if (++itile == ntq) {
       itile = t0;
-      ++ihead;
+      qp += p.q.sh - back * p.q.st;
+      gp += p.dout.sh - back * p.dout.st;
+      sp += p.Sq - back;
     }
   };
   int ctile = t0;  // of the step to compute
-  auto step = [&](const uint16_t* qt, const uint16_t* gt, const RowStats& rs) {
+  auto step = [&](const uint16_t* qt, const uint16_t* gt, const float* stats) {
     const int r0 = ctile * kTile;
     if (++ctile == ntq) ctile = t0;
     if (first >= w.lk) return;
-    if (!p.causal || r0 + off >= first + kCols - 1)
-      dkv_tile<DP, false>(st, qt, gt, rs, f, 0, half);
-    else if (r0 + kTile - 1 + off >= first)
-      dkv_tile<DP, true>(st, qt, gt, rs, f, rowc - off - r0, half);
+    if (p.causal && r0 + kTile - 1 + off < first) return;
+    const bool mask = p.causal && r0 + off < first + kCols - 1;
+    dkv_tile<DP>(st, qt, gt, stats, w.lq - r0, f, mask, rowc - off - r0, half, lane);
   };
-  if (nt > 0) issue(q0, g0);
+  if (nt > 0) issue(q0, g0, s0);
   for (int n = 0; n < nt; n += 2) {
-    RowStats rs = nrs;
     tiles_ready();
-    if (n + 1 < nt) issue(q1, g1);
-    step(q0, g0, rs);
+    if (n + 1 < nt) issue(q1, g1, s1);
+    step(q0, g0, s0);
     if (n + 1 >= nt) break;
-    rs = nrs;
     tiles_ready();
-    if (n + 2 < nt) issue(q0, g0);
-    step(q1, g1, rs);
+    if (n + 2 < nt) issue(q0, g0, s0);
+    step(q1, g1, s1);
   }
   if (row < w.lk) {
     store_cols<DP>(p.dk.p + w.batch * p.dk.sb + krow * p.dk.st + w.head * p.dk.sh, st.dk, p.scale,

@@ -38,7 +38,7 @@ __device__ __forceinline__ void fwd_tile(FwdState<DP>& st, const uint16_t* kt, c
 #pragma unroll
   for (int i = 0; i < Geo<DP>::kSteps; ++i)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) s[r] = mfma32(read_rows<DP>(kt, f, i, r), st.q[i], s[r]);
+    for (int r = 0; r < 2; ++r) s[r] = mfma32(read_rows<DP>(kt, f.row, i, r), st.q[i], s[r]);
   float top = -kInf;
 #pragma unroll
   for (int r = 0; r < 2; ++r)
@@ -73,7 +73,7 @@ __device__ __forceinline__ void fwd_tile(FwdState<DP>& st, const uint16_t* kt, c
   for (int b = 0; b < 4; ++b) {
     const bf16x8 pb = pack8(s[b >> 1], b & 1);
 #pragma unroll
-    for (int t = 0; t < Geo<DP>::kDT; ++t) st.o[t] = mfma32(read_tr<DP>(vt, f, t, b), pb, st.o[t]);
+    for (int t = 0; t < Geo<DP>::kDT; ++t) st.o[t] = mfma32(read_tr<DP>(vt, f.tr, t, b), pb, st.o[t]);
   }
 }
 
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_fwd(AttnArgs p, int64_t
   __shared__ __attribute__((aligned(16))) uint16_t k1[Geo<DP>::kElems], v1[Geo<DP>::kElems];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Work w = find_work<false>(p, xcd_order(blockIdx.x, gridDim.x), slots, p.H);
+  const Work w = find_work<false>(p, slots, p.H);
   if (!w.valid) return;
   // causal: the tiles with the most keys first
   const int tile = p.causal ? w.ntiles - 1 - w.tile : w.tile;
@@ -105,10 +105,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_fwd(AttnArgs p, int64_t
   for (int t = 0; t < Geo<DP>::kDT; ++t) st.o[t] = f32x16{};
   st.m = -kInf;
   st.l = 0.0f;
-  st.c = p.scale * kLog2e;
+  st.c = uniform(p.scale * kLog2e);
   const FragOff f = frag_off<DP>(lane);
-  TileLoader<DP> ld;
-  tile_loader<DP>(ld, p.D, wave, lane);
+  const TileLoader ld = tile_loader<DP>(p.D, wave, lane);
 
   // keys that any query of the workgroup sees
   int keys = w.lk;
@@ -131,21 +130,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_fwd(AttnArgs p, int64_t
       fwd_tile<DP, true>(st, kt, vt, f, mine - r0, half);
   };
   if (nt > 0) {
-    load_tile<DP>(k0, ld, kb, p.k.st, 0, w.lk, wave);
-    load_tile<DP>(v0, ld, vb, p.v.st, 0, w.lk, wave);
+    load_tile<DP>(k0, ld, kb, p.k.st, w.lk, wave);
+    load_tile<DP>(v0, ld, vb, p.v.st, w.lk, wave);
   }
   for (int j = 0; j < nt; j += 2) {
     tiles_ready();
     if (j + 1 < nt) {
-      load_tile<DP>(k1, ld, kb, p.k.st, (j + 1) * kTile, w.lk, wave);
-      load_tile<DP>(v1, ld, vb, p.v.st, (j + 1) * kTile, w.lk, wave);
+      load_tile<DP>(k1, ld, kb + (j + 1) * (kTile * p.k.st), p.k.st, w.lk - (j + 1) * kTile, wave);
+      load_tile<DP>(v1, ld, vb + (j + 1) * (kTile * p.v.st), p.v.st, w.lk - (j + 1) * kTile, wave);
     }
     step(k0, v0, j);
     if (j + 1 >= nt) break;
     tiles_ready();
     if (j + 2 < nt) {
-      load_tile<DP>(k0, ld, kb, p.k.st, (j + 2) * kTile, w.lk, wave);
-      load_tile<DP>(v0, ld, vb, p.v.st, (j + 2) * kTile, w.lk, wave);
+      load_tile<DP>(k0, ld, kb + (j + 2) * (kTile * p.k.st), p.k.st, w.lk - (j + 2) * kTile, wave);
+      load_tile<DP>(v0, ld, vb + (j + 2) * (kTile * p.v.st), p.v.st, w.lk - (j + 2) * kTile, wave);
     }
     step(k1, v1, j + 1);
   }
