@@ -499,10 +499,14 @@ typedef struct qlora_attention_t {
  * A query that sees no key gets O = 0 and lse = -inf.  Sums and the softmax
  * are fp32; the probabilities are rounded to bf16 for the product with V.
  * Values outside a sequence never reach its outputs, whatever they are; a
- * NaN or infinity inside one may reach every row of that sequence and head. */
+ * NaN or infinity inside one may reach every row of that sequence and head.
+ * ws_bytes >= qlora_attention_fwd_workspace_size(a) (16-byte aligned; 0, and
+ * ws may be NULL, where the work is not split: see the backward pass). */
+size_t qlora_attention_fwd_workspace_size(const qlora_attention_t* a);
 int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
                             const qlora_heads_t* k, const qlora_heads_t* v,
-                            const qlora_heads_t* o, float* lse, hipStream_t stream);
+                            const qlora_heads_t* o, float* lse, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
 
 /* qlora_attention_bwd -- the gradients of q, k and v for the output gradient
  * dout, with the probabilities recomputed from lse (o and lse as the forward
@@ -512,8 +516,11 @@ int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
  * dK and dV summed over the query heads of a key/value head.  dq, dk and dv
  * are overwritten; queries that see no key, and keys that no query sees, get
  * 0.  P and dS are rounded to bf16 for the products that follow.
- * ws_bytes >= qlora_attention_bwd_workspace_size(a) (0 for invalid sizes or
- * no queries; ws may then be NULL). */
+ * ws_bytes >= qlora_attention_bwd_workspace_size(a) (16-byte aligned; 0 for
+ * invalid sizes or nothing to compute).  Both calls split long walks over
+ * several workgroups where that is faster (few tiles, or few key/value heads
+ * under a causal mask), by the shapes alone; the workspace then holds their
+ * fp32 partial results, and a second kernel adds them in a fixed order. */
 size_t qlora_attention_bwd_workspace_size(const qlora_attention_t* a);
 int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
                             const qlora_heads_t* k, const qlora_heads_t* v,

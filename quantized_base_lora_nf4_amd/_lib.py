@@ -62,6 +62,7 @@ EXPORTS = (
     "qlora_config_error_workspace_size",
     "qlora_config_error",
     "qlora_attention_fwd",
+    "qlora_attention_fwd_workspace_size",
     "qlora_attention_bwd",
     "qlora_attention_bwd_workspace_size",
     "qlora_norm_fwd",
@@ -189,7 +190,9 @@ def lib() -> ctypes.CDLL:
     L.qlora_ilp_plan.argtypes = [i32, i32, vp, vp, i64, vp, vp, vp]
     pa, ph = ctypes.POINTER(Attention), ctypes.POINTER(Heads)
     L.qlora_attention_fwd.restype = i32
-    L.qlora_attention_fwd.argtypes = [pa, ph, ph, ph, ph, vp, vp]
+    L.qlora_attention_fwd.argtypes = [pa, ph, ph, ph, ph, vp, vp, sz, vp]
+    L.qlora_attention_fwd_workspace_size.restype = sz
+    L.qlora_attention_fwd_workspace_size.argtypes = [pa]
     L.qlora_attention_bwd_workspace_size.restype = sz
     L.qlora_attention_bwd_workspace_size.argtypes = [pa]
     L.qlora_attention_bwd.restype = i32

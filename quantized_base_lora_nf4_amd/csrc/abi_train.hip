@@ -123,7 +123,8 @@ extern "C" {
 
 int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
                             const qlora_heads_t* k, const qlora_heads_t* v,
-                            const qlora_heads_t* o, float* lse, hipStream_t stream) {
+                            const qlora_heads_t* o, float* lse, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
   const int32_t ok = attn_ok(a);
   if (ok != QLORA_OK) return ok;
   const int64_t nq = stat_rows(a), nk = a->cu_seqlens_q || a->n_seq > 0 ? a->k_rows : 0;
@@ -132,16 +133,23 @@ int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
   if (nq == 0) return QLORA_OK;
   if (!lse || !aligned(lse, 4)) return QLORA_ERR_INVALID;
   AttnArgs r = attn_args(a);
+  const size_t need = (size_t)attn_fwd_workspace(r) * 4;
+  if (need > 0 && (!ws || !aligned(ws, 16))) return QLORA_ERR_INVALID;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
   r.q = view(q);
   r.k = view(k);
   r.v = view(v);
   r.o = view(o);
   r.lse = lse;
-  return launch_status(launch_attn_fwd(r, stream));
+  return launch_status(launch_attn_fwd(r, static_cast<float*>(ws), stream));
+}
+
+size_t qlora_attention_fwd_workspace_size(const qlora_attention_t* a) {
+  return attn_ok(a) == QLORA_OK ? (size_t)attn_fwd_workspace(attn_args(a)) * 4 : 0;
 }
 
 size_t qlora_attention_bwd_workspace_size(const qlora_attention_t* a) {
-  return attn_ok(a) == QLORA_OK ? (size_t)stat_rows(a) * 4 : 0;
+  return attn_ok(a) == QLORA_OK ? (size_t)attn_bwd_workspace(attn_args(a)) * 4 : 0;
 }
 
 int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
@@ -157,11 +165,11 @@ int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
       !view_ok(k, nk) || !view_ok(v, nk) || !view_ok(dk, nk) || !view_ok(dv, nk))
     return QLORA_ERR_INVALID;
   if (nq == 0 && nk == 0) return QLORA_OK;
-  if (nq > 0) {
-    if (!lse || !aligned(lse, 4) || !ws || !aligned(ws, 16)) return QLORA_ERR_INVALID;
-    if (ws_bytes < (size_t)nq * 4) return QLORA_ERR_WORKSPACE;
-  }
+  if (nq > 0 && (!lse || !aligned(lse, 4))) return QLORA_ERR_INVALID;
   AttnArgs r = attn_args(a);
+  const size_t need = (size_t)attn_bwd_workspace(r) * 4;
+  if (need > 0 && (!ws || !aligned(ws, 16))) return QLORA_ERR_INVALID;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
   r.q = view(q);
   r.k = view(k);
   r.v = view(v);
@@ -171,8 +179,7 @@ int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
   r.dk = view(dk);
   r.dv = view(dv);
   r.lse = const_cast<float*>(lse);
-  r.delta = static_cast<float*>(ws);
-  return launch_status(launch_attn_bwd(r, stream));
+  return launch_status(launch_attn_bwd(r, static_cast<float*>(ws), stream));
 }
 
 int32_t qlora_norm_fwd(const void* x, int64_t rows, int64_t width, int32_t x_type,

@@ -34,6 +34,8 @@ constexpr int kWaves = 4;    // waves per workgroup
 constexpr int kCols = 32;    // columns per wave
 constexpr int kBlock = kWaves * kCols;  // columns per workgroup
 
+constexpr unsigned kResident = 512;     // workgroups that run at once: two on each of 256 CUs
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
@@ -47,6 +49,7 @@ struct Work {
   int64_t q0, k0;          // first query and key row of the sequence (packed; dense: 0)
   int lq, lk;              // lengths
   int tile, ntiles;        // tile of kBlock columns, and how many the sequence has
+  int split;               // which share of the walk over the other side
   bool valid;
 };
 
@@ -57,17 +60,17 @@ struct Work {
 // slots that take longest come first for all heads, and the last workgroups
 // to start are short ones.
 struct Place {
-  int64_t head, slot;
+  unsigned head, slot;
 };
-__device__ __forceinline__ Place place_of(int64_t id, int64_t heads, int64_t slots) {
+__device__ __forceinline__ Place place_of(unsigned id, unsigned heads) {
   Place p;
   if (heads % 8 == 0) {
-    const int64_t per = heads >> 3, j = id >> 3;
-    p.head = (id & 7) * per + j % per;
+    const unsigned per = heads >> 3, j = id >> 3;
     p.slot = j / per;
+    p.head = (id & 7) * per + (j - p.slot * per);
   } else {
-    p.head = id % heads;
     p.slot = id / heads;
+    p.head = id - p.slot * heads;
   }
   return p;
 }
@@ -85,18 +88,23 @@ __device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
 // ones give wrong results but no access out of range.
 // kKeys: the columns are keys (the dK/dV kernel), else queries.
 template <bool kKeys>
-__device__ __forceinline__ Work find_work(const AttnArgs& p, int64_t slots, int heads) {
+__device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned heads) {
   Work w;
-  const Place at = place_of(blockIdx.x, gridDim.x / slots, slots);
-  w.head = (int)(at.head % heads);
-  const int64_t slot = at.slot;
+  // heads of the whole batch, times splits, is below 2^31 (the grid's size)
+  const unsigned all = heads * (p.cu_q ? 1u : (unsigned)p.nseq) * (unsigned)p.splits;
+  const Place at = place_of(blockIdx.x, all);
+  const unsigned head = at.head / (unsigned)p.splits;
+  w.split = (int)(at.head - head * (unsigned)p.splits);
+  const unsigned batch = head / heads;
+  w.head = (int)(head - batch * heads);
+  const int slot = (int)at.slot;
   if (!p.cu_q) {
-    w.batch = at.head / heads;
+    w.batch = batch;
     w.q0 = w.k0 = 0;
     w.lq = (int)p.Sq;
     w.lk = (int)p.Sk;
-    w.tile = (int)slot;
-    w.ntiles = (int)slots;
+    w.tile = slot;
+    w.ntiles = slots;
     w.valid = true;
     return w;
   }
@@ -105,7 +113,7 @@ __device__ __forceinline__ Work find_work(const AttnArgs& p, int64_t slots, int 
   const int lane = threadIdx.x & 63;
   const int32_t* cu = kKeys ? p.cu_k : p.cu_q;
   const int64_t rows = kKeys ? p.Sk : p.Sq;
-  int64_t base = 0;
+  int base = 0;
   for (int s0 = 0; s0 <= p.nseq; s0 += 64) {
     const int s = s0 + lane;
     int n = 0;
@@ -125,7 +133,7 @@ __device__ __forceinline__ Work find_work(const AttnArgs& p, int64_t slots, int 
       const int l = __ffsll((unsigned long long)past) - 1;
       const int sq = __builtin_amdgcn_readfirstlane(s0 + l);
       w.ntiles = __builtin_amdgcn_readfirstlane(__shfl(n, l, 64));
-      w.tile = (int)(slot - base) - __builtin_amdgcn_readfirstlane(__shfl(sum - n, l, 64));
+      w.tile = slot - base - __builtin_amdgcn_readfirstlane(__shfl(sum - n, l, 64));
       const bool none = sq == p.nseq;
       w.q0 = clamp_row(p.cu_q[sq], 0, p.Sq);
       w.k0 = clamp_row(p.cu_k[sq], 0, p.Sk);
@@ -297,6 +305,27 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* tile, int tr, int d, i
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Tile rows 32 rt .. times xb; operands are read two steps before their use.
+template <int DP>
+__device__ __forceinline__ f32x16 rows_times(const uint16_t* tile,
+                                             const bf16x8 (&xb)[Geo<DP>::kSteps], const FragOff& f,
+                                             int rt) {
+  constexpr int N = Geo<DP>::kSteps, kAhead = 2;
+  const int row = opaque(f.row);
+  f32x16 acc = f32x16{};
+  bf16x8 x[N];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = read_rows<DP>(tile, row, i, rt);
+  step_fence();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + kAhead < N) x[i + kAhead] = read_rows<DP>(tile, row, i + kAhead, rt);
+    acc = mfma32(x[i], xb[i], acc);
+    step_fence();
+  }
+  return acc;
+}
+
 // The register operand: row `r` (per lane) of a matrix, dimensions
 // 16 s + 8 (lane / 32) + 0..7 in element s, zeros past D.
 template <int DP>
@@ -331,6 +360,22 @@ __device__ __forceinline__ void store_cols(uint16_t* out, const f32x16 (&acc)[Ge
     }
 }
 
+// The same in fp32, for a partial result.
+template <int DP>
+__device__ __forceinline__ void store_cols(float* out, const f32x16 (&acc)[Geo<DP>::kDT],
+                                           float mul, int D, int lane) {
+#pragma unroll
+  for (int t = 0; t < Geo<DP>::kDT; ++t)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int d = 32 * t + 16 * (a >> 1) + 8 * (lane >> 5) + 4 * (a & 1);
+      if (d < D)
+        *reinterpret_cast<f32x4*>(out + d) =
+            f32x4{acc[t][4 * a] * mul, acc[t][4 * a + 1] * mul, acc[t][4 * a + 2] * mul,
+                  acc[t][4 * a + 3] * mul};
+    }
+}
+
 // Elements 8 s .. 8 s + 7 of a score accumulator as the B operand of a
 // 16-deep product.
 __device__ __forceinline__ bf16x8 pack8(const f32x16& x, int s) {
@@ -348,6 +393,91 @@ __device__ __forceinline__ int elem_row(int v, int half) {
 // The other half's value (lane ^ 32).
 __device__ __forceinline__ float other_half(float x) {
   return __shfl_xor(x, 32, 64);
+}
+
+// One tile of queries in the forward and the dQ kernel.
+struct Queries {
+  int off;                 // causal: query i sees keys 0 .. i + off
+  int first, row, rowc;    // this wave's first query, this lane's, and that or the last one
+  int seen_first, seen_last, mine;  // last key seen by the wave's first, by its last, by this lane's
+  int t0, t1;              // tiles of keys to walk over (of this split)
+  const uint16_t* k;
+  const uint16_t* v;
+};
+
+__device__ __forceinline__ Queries query_tile(const AttnArgs& p, const Work& w, int wave,
+                                              int lane) {
+  Queries t;
+  // causal: the tiles with the most keys first
+  const int tile = p.causal ? w.ntiles - 1 - w.tile : w.tile;
+  const int col0 = tile * kBlock;
+  t.off = w.lk - w.lq;
+  t.first = col0 + wave * kCols;
+  t.row = t.first + (lane & 31);
+  t.rowc = t.row < w.lq ? t.row : w.lq - 1;
+  int keys = w.lk;
+  t.seen_first = t.seen_last = t.mine = w.lk - 1;
+  if (p.causal) {
+    const int e = (col0 + kBlock < w.lq ? col0 + kBlock : w.lq) + t.off;
+    keys = e < keys ? (e > 0 ? e : 0) : keys;
+    if (t.first + t.off < t.seen_first) t.seen_first = t.first + t.off;
+    if (t.first + kCols - 1 + t.off < t.seen_last) t.seen_last = t.first + kCols - 1 + t.off;
+    if (t.rowc + t.off < t.mine) t.mine = t.rowc + t.off;
+  }
+  const int nt = (keys + kTile - 1) / kTile;
+  t.t0 = (int)((int64_t)nt * w.split / p.splits);
+  t.t1 = (int)((int64_t)nt * (w.split + 1) / p.splits);
+  const int hk = w.head / (p.H / p.Hkv);
+  t.k = p.k.p + w.batch * p.k.sb + (w.k0 + (int64_t)t.t0 * kTile) * p.k.st + hk * p.k.sh;
+  t.v = p.v.p + w.batch * p.v.sb + (w.k0 + (int64_t)t.t0 * kTile) * p.v.st + hk * p.v.sh;
+  return t;
+}
+
+// Calls tile(K tile, V tile, mask, last) for the tiles of keys that any of the
+// wave's queries sees (mask: not all rows of the tile in some lane; this
+// lane's query sees rows 0 .. last).  Two buffers each: a tile's loads run
+// during the step before it.  The first tile's loads are issued by
+// start_keys, before whatever else the kernel loads.
+template <int DP>
+struct KeyBuffers {
+  uint16_t *k0, *v0, *k1, *v1;
+};
+
+template <int DP>
+__device__ __forceinline__ void start_keys(const KeyBuffers<DP>& b, const AttnArgs& p,
+                                           const Work& w, const Queries& t, const TileLoader& ld,
+                                           int wave) {
+  if (t.t0 < t.t1) {
+    load_tile<DP>(b.k0, ld, t.k, p.k.st, w.lk - t.t0 * kTile, wave);
+    load_tile<DP>(b.v0, ld, t.v, p.v.st, w.lk - t.t0 * kTile, wave);
+  }
+}
+
+template <int DP, class F>
+__device__ __forceinline__ void walk_keys(const KeyBuffers<DP>& b, const AttnArgs& p,
+                                          const Work& w, Queries& t, const TileLoader& ld,
+                                          int wave, F&& tile) {
+  auto issue = [&](uint16_t* kt, uint16_t* vt, int j) {
+    t.k += kTile * p.k.st;
+    t.v += kTile * p.v.st;
+    load_tile<DP>(kt, ld, t.k, p.k.st, w.lk - j * kTile, wave);
+    load_tile<DP>(vt, ld, t.v, p.v.st, w.lk - j * kTile, wave);
+  };
+  auto step = [&](const uint16_t* kt, const uint16_t* vt, int j) {
+    const int r0 = j * kTile;
+    if (t.first >= w.lq || r0 > t.seen_last) return;
+    const bool mask = r0 + kTile - 1 > t.seen_first;
+    tile(kt, vt, mask, t.mine - r0);
+  };
+  for (int j = t.t0; j < t.t1; j += 2) {
+    tiles_ready();
+    if (j + 1 < t.t1) issue(b.k1, b.v1, j + 1);
+    step(b.k0, b.v0, j);
+    if (j + 1 >= t.t1) break;
+    tiles_ready();
+    if (j + 2 < t.t1) issue(b.k0, b.v0, j + 2);
+    step(b.k1, b.v1, j + 1);
+  }
 }
 
 }  // namespace attn

@@ -63,27 +63,6 @@ __device__ __forceinline__ void scores(f32x16& acc_x, f32x16& acc_y, const uint1
   }
 }
 
-// Tile rows 32 rt .. times xb; operands are read two steps before their use.
-template <int DP>
-__device__ __forceinline__ f32x16 rows_times(const uint16_t* tile,
-                                             const bf16x8 (&xb)[Geo<DP>::kSteps], const FragOff& f,
-                                             int rt) {
-  constexpr int N = Geo<DP>::kSteps, kAhead = 2;
-  const int row = opaque(f.row);
-  f32x16 acc = f32x16{};
-  bf16x8 x[N];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) x[i] = read_rows<DP>(tile, row, i, rt);
-  step_fence();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i + kAhead < N) x[i + kAhead] = read_rows<DP>(tile, row, i + kAhead, rt);
-    acc = mfma32(x[i], xb[i], acc);
-    step_fence();
-  }
-  return acc;
-}
-
 // One tile of keys; this lane's query sees tile rows 0 .. last (mask: not
 // all of them in some lane).
 template <int DP>
@@ -119,27 +98,23 @@ __device__ __forceinline__ void dq_tile(DqState<DP>& st, const uint16_t* kt, con
 }
 
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dq(AttnArgs p, int64_t slots) {
+__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dq(AttnArgs p, int slots) {
   __shared__ __attribute__((aligned(16))) uint16_t k0[Geo<DP>::kElems], v0[Geo<DP>::kElems];
   __shared__ __attribute__((aligned(16))) uint16_t k1[Geo<DP>::kElems], v1[Geo<DP>::kElems];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Work w = find_work<false>(p, slots, p.H);
   if (!w.valid) return;
-  const int tile = p.causal ? w.ntiles - 1 - w.tile : w.tile;
-  const int col0 = tile * kBlock;
-  if (col0 >= w.lq) return;
-  const int off = w.lk - w.lq;
-  const int hk = w.head / (p.H / p.Hkv);
-  const uint16_t* kb = p.k.p + w.batch * p.k.sb + w.k0 * p.k.st + hk * p.k.sh;
-  const uint16_t* vb = p.v.p + w.batch * p.v.sb + w.k0 * p.v.st + hk * p.v.sh;
+  Queries t = query_tile(p, w, wave, lane);
+  if (t.first - wave * kCols >= w.lq) return;
+  const TileLoader ld = tile_loader<DP>(p.D, wave, lane);
+  const KeyBuffers<DP> buf{k0, v0, k1, v1};
+  start_keys<DP>(buf, p, w, t, ld, wave);
 
-  const int first = col0 + wave * kCols;
-  const int row = first + (lane & 31);
-  const int rowc = row < w.lq ? row : w.lq - 1;
-  const int64_t qrow = w.q0 + rowc;
+  const int64_t qrow = w.q0 + t.rowc;
   const int64_t stat = (w.batch * p.H + w.head) * p.Sq + qrow;
   DqState<DP> st;
+  const float lse = p.lse[stat];
   load_cols<DP>(st.q, p.q.p + w.batch * p.q.sb + qrow * p.q.st + w.head * p.q.sh, p.D, lane);
   load_cols<DP>(st.g, p.dout.p + w.batch * p.dout.sb + qrow * p.dout.st + w.head * p.dout.sh, p.D,
                 lane);
@@ -153,55 +128,23 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dq(AttnArgs p, int6
       for (int e = 0; e < 8; ++e) d = fmaf((float)st.g[i][e], (float)o[i][e], d);
     st.delta = d + other_half(d);
   }
-  if (half == 0 && row < w.lq) p.delta[stat] = st.delta;
-  const float lse = p.lse[stat];
+  if (half == 0 && t.row < w.lq && w.split == 0) p.delta[stat] = st.delta;
   st.lse = lse == -kInf ? kInf : lse * kLog2e;
   st.c = uniform(p.scale * kLog2e);
 #pragma unroll
-  for (int t = 0; t < Geo<DP>::kDT; ++t) st.dq[t] = f32x16{};
+  for (int i = 0; i < Geo<DP>::kDT; ++i) st.dq[i] = f32x16{};
   const FragOff f = frag_off<DP>(lane);
-  const TileLoader ld = tile_loader<DP>(p.D, wave, lane);
-
-  int keys = w.lk;
-  if (p.causal) {
-    const int e = (col0 + kBlock < w.lq ? col0 + kBlock : w.lq) + off;
-    keys = e < keys ? (e > 0 ? e : 0) : keys;
-  }
-  const int nt = (keys + kTile - 1) / kTile;
-  const int seen_first = p.causal ? first + off : w.lk - 1;
-  int seen_last = w.lk - 1, mine = w.lk - 1;
-  if (p.causal) {
-    if (first + kCols - 1 + off < seen_last) seen_last = first + kCols - 1 + off;
-    if (rowc + off < mine) mine = rowc + off;
-  }
-  auto step = [&](const uint16_t* kt, const uint16_t* vt, int j) {
-    const int r0 = j * kTile;
-    if (first >= w.lq || r0 > seen_last) return;
-    const bool mask = r0 + kTile - 1 > seen_first || r0 + kTile > w.lk;
-    dq_tile<DP>(st, kt, vt, f, mask, mine - r0, half);
-  };
-  if (nt > 0) {
-    load_tile<DP>(k0, ld, kb, p.k.st, w.lk, wave);
-    load_tile<DP>(v0, ld, vb, p.v.st, w.lk, wave);
-  }
-  for (int j = 0; j < nt; j += 2) {
-    tiles_ready();
-    if (j + 1 < nt) {
-      load_tile<DP>(k1, ld, kb + (j + 1) * (kTile * p.k.st), p.k.st, w.lk - (j + 1) * kTile, wave);
-      load_tile<DP>(v1, ld, vb + (j + 1) * (kTile * p.v.st), p.v.st, w.lk - (j + 1) * kTile, wave);
-    }
-    step(k0, v0, j);
-    if (j + 1 >= nt) break;
-    tiles_ready();
-    if (j + 2 < nt) {
-      load_tile<DP>(k0, ld, kb + (j + 2) * (kTile * p.k.st), p.k.st, w.lk - (j + 2) * kTile, wave);
-      load_tile<DP>(v0, ld, vb + (j + 2) * (kTile * p.v.st), p.v.st, w.lk - (j + 2) * kTile, wave);
-    }
-    step(k1, v1, j + 1);
-  }
-  if (row < w.lq)
+  walk_keys<DP>(buf, p, w, t, ld, wave,
+                [&](const uint16_t* kt, const uint16_t* vt, bool mask, int last) {
+                  dq_tile<DP>(st, kt, vt, f, mask, last, half);
+                });
+  if (t.row >= w.lq) return;
+  if (p.splits == 1)
     store_cols<DP>(p.dq.p + w.batch * p.dq.sb + qrow * p.dq.st + w.head * p.dq.sh, st.dq, p.scale,
                    p.D, lane);
+  else
+    store_cols<DP>(p.part + (w.split * p.all + stat) * p.D, st.dq,
+                   1.0f, p.D, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -286,7 +229,7 @@ __device__ __forceinline__ void dkv_tile(DkvState<DP>& st, const uint16_t* qt, c
 }
 
 template <int DP>
-__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int64_t slots) {
+__global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int slots) {
   __shared__ __attribute__((aligned(16))) uint16_t q0[Geo<DP>::kElems], g0[Geo<DP>::kElems];
   __shared__ __attribute__((aligned(16))) uint16_t q1[Geo<DP>::kElems], g1[Geo<DP>::kElems];
   __shared__ float s0[2 * kTile], s1[2 * kTile];  // lse, then D, of the tile's rows
@@ -294,10 +237,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Work w = find_work<true>(p, slots, p.Hkv);
   if (!w.valid) return;
-  // causal: the first keys are seen by the most queries, so they come first;
-  // from the middle on, the last tiles come first.
+  // causal: the first keys are seen by the most queries, so they come first.
+  // Where all workgroups start at once, two to a CU, the second half goes the
+  // other way: the CU with the longest of the first half gets the shortest.
   const int mid = (w.ntiles + 1) / 2;
-  const int tile = p.causal && w.tile >= mid ? w.ntiles - 1 - (w.tile - mid) : w.tile;
+  const bool resident = gridDim.x <= kResident;
+  const int tile =
+      p.causal && resident && w.tile >= mid ? w.ntiles - 1 - (w.tile - mid) : w.tile;
   const int col0 = tile * kBlock;
   if (col0 >= w.lk) return;
   const int off = w.lk - w.lq;       // query i sees keys 0 .. i + off
@@ -307,17 +253,6 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
   const int row = first + (lane & 31);
   const int rowc = row < w.lk ? row : w.lk - 1;
   const int64_t krow = w.k0 + rowc;
-  DkvState<DP> st;
-  load_cols<DP>(st.k, p.k.p + w.batch * p.k.sb + krow * p.k.st + w.head * p.k.sh, p.D, lane);
-  load_cols<DP>(st.v, p.v.p + w.batch * p.v.sb + krow * p.v.st + w.head * p.v.sh, p.D, lane);
-#pragma unroll
-  for (int t = 0; t < Geo<DP>::kDT; ++t) {
-    st.dk[t] = f32x16{};
-    st.dv[t] = f32x16{};
-  }
-  st.c = uniform(p.scale * kLog2e);
-  st.inv_scale = uniform(1.0f / p.scale);
-  const FragOff f = frag_off<DP>(lane);
   const TileLoader ld = tile_loader<DP>(p.D, wave, lane);
 
   // tiles of queries that see any of the workgroup's keys
@@ -325,16 +260,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
   int t0 = 0;
   if (p.causal && col0 - off > 0) t0 = (col0 - off) / kTile;
   const int per = ntq > t0 ? ntq - t0 : 0;
-  const int nt = per * share;
+  const int n0 = (int)((int64_t)per * share * w.split / p.splits);
+  const int n1 = (int)((int64_t)per * share * (w.split + 1) / p.splits);
   // Step n: query tile t0 + n % per of head n / per of the group.  The
   // pointers are those of the next step to issue.
-  const int head0 = w.head * share;
-  const int64_t row0 = w.q0 + (int64_t)t0 * kTile;
+  int itile = t0 + (per ? n0 % per : 0);
+  const int head0 = w.head * share + (per ? n0 / per : 0);
+  const int64_t row0 = w.q0 + (int64_t)itile * kTile;
   const uint16_t* qp = p.q.p + w.batch * p.q.sb + row0 * p.q.st + head0 * p.q.sh;
   const uint16_t* gp = p.dout.p + w.batch * p.dout.sb + row0 * p.dout.st + head0 * p.dout.sh;
   const float* sp = (wave & 1 ? p.delta : p.lse) + (w.batch * p.H + head0) * p.Sq + row0;
   const int64_t back = (int64_t)per * kTile;  // from the end of a head's rows to their start
-  int itile = t0;
+  int ctile = itile;  // of the step to compute
   auto issue = [&](uint16_t* qb, uint16_t* gb, float* sb) {
     const int left = w.lq - itile * kTile;
     load_tile<DP>(qb, ld, qp, p.q.st, left, wave);
@@ -354,7 +291,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
       sp += p.Sq - back;
     }
   };
-  int ctile = t0;  // of the step to compute
+  if (n0 < n1) issue(q0, g0, s0);
+  DkvState<DP> st;
+  load_cols<DP>(st.k, p.k.p + w.batch * p.k.sb + krow * p.k.st + w.head * p.k.sh, p.D, lane);
+  load_cols<DP>(st.v, p.v.p + w.batch * p.v.sb + krow * p.v.st + w.head * p.v.sh, p.D, lane);
+#pragma unroll
+  for (int t = 0; t < Geo<DP>::kDT; ++t) {
+    st.dk[t] = f32x16{};
+    st.dv[t] = f32x16{};
+  }
+  st.c = uniform(p.scale * kLog2e);
+  st.inv_scale = uniform(1.0f / p.scale);
+  const FragOff f = frag_off<DP>(lane);
   auto step = [&](const uint16_t* qt, const uint16_t* gt, const float* stats) {
     const int r0 = ctile * kTile;
     if (++ctile == ntq) ctile = t0;
@@ -363,17 +311,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
     const bool mask = p.causal && r0 + off < first + kCols - 1;
     dkv_tile<DP>(st, qt, gt, stats, w.lq - r0, f, mask, rowc - off - r0, half, lane);
   };
-  if (nt > 0) issue(q0, g0, s0);
-  for (int n = 0; n < nt; n += 2) {
+  for (int n = n0; n < n1; n += 2) {
     tiles_ready();
-    if (n + 1 < nt) issue(q1, g1, s1);
+    if (n + 1 < n1) issue(q1, g1, s1);
     step(q0, g0, s0);
-    if (n + 1 >= nt) break;
+    if (n + 1 >= n1) break;
     tiles_ready();
-    if (n + 2 < nt) issue(q0, g0, s0);
+    if (n + 2 < n1) issue(q0, g0, s0);
     step(q1, g1, s1);
   }
-  if (row < w.lk) {
+  if (row >= w.lk) return;
+  if (p.splits > 1) {
+    const int64_t at = w.split * p.all + (w.batch * p.Hkv + w.head) * p.Sk + krow;
+    store_cols<DP>(p.part + at * p.D, st.dk, 1.0f, p.D, lane);
+    store_cols<DP>(p.part + (p.splits * p.all + at) * p.D, st.dv, 1.0f, p.D, lane);
+  } else {
     store_cols<DP>(p.dk.p + w.batch * p.dk.sb + krow * p.dk.st + w.head * p.dk.sh, st.dk, p.scale,
                    p.D, lane);
     store_cols<DP>(p.dv.p + w.batch * p.dv.sb + krow * p.dv.st + w.head * p.dv.sh, st.dv, 1.0f,
@@ -382,26 +334,42 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
 }
 
 template <int DP>
-hipError_t launch_bwd(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_bwd(AttnArgs a, hipStream_t stream) {
   const int64_t nb = a.cu_q ? 1 : a.nseq;
+  hipError_t e = hipSuccess;
   if (a.Sq > 0) {
+    a.splits = attn_splits(a, kAttnDq);
+    a.all = a.Sq * a.H * nb;
     const int64_t slots = tile_slots(a, a.Sq);
-    k_attn_bwd_dq<DP><<<(unsigned)(slots * a.H * nb), kWaves * 64, 0, stream>>>(a, slots);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    k_attn_bwd_dq<DP>
+        <<<(unsigned)(slots * a.H * nb * a.splits), kWaves * 64, 0, stream>>>(a, (int)slots);
+    e = hipGetLastError();
+    if (e == hipSuccess && a.splits > 1)
+      e = launch_attn_join_sum(a, 1, &a.dq, &a.scale, a.Sq, a.H, stream);
   }
-  if (a.Sk > 0) {
+  if (e == hipSuccess && a.Sk > 0) {
+    a.splits = attn_splits(a, kAttnDkv);
+    a.all = a.Sk * a.Hkv * nb;
     const int64_t slots = tile_slots(a, a.Sk);
-    k_attn_bwd_dkv<DP><<<(unsigned)(slots * a.Hkv * nb), kWaves * 64, 0, stream>>>(a, slots);
-    return hipGetLastError();
+    k_attn_bwd_dkv<DP>
+        <<<(unsigned)(slots * a.Hkv * nb * a.splits), kWaves * 64, 0, stream>>>(a, (int)slots);
+    e = hipGetLastError();
+    if (e == hipSuccess && a.splits > 1) {
+      const AttnView out[2] = {a.dk, a.dv};
+      const float mul[2] = {a.scale, 1.0f};
+      e = launch_attn_join_sum(a, 2, out, mul, a.Sk, a.Hkv, stream);
+    }
   }
-  return hipSuccess;
+  return e;
 }
 
 }  // namespace
 
-hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_attn_bwd(const AttnArgs& args, float* ws, hipStream_t stream) {
+  AttnArgs a = args;
   if (!a.cu_q && a.nseq == 0) return hipSuccess;
+  a.delta = ws;
+  a.part = ws + (a.Sq * a.H * (a.cu_q ? 1 : a.nseq) + 3) / 4 * 4;
   return a.D <= 64 ? launch_bwd<64>(a, stream) : launch_bwd<128>(a, stream);
 }
 

@@ -163,7 +163,7 @@ struct ClipArgs {
 };
 hipError_t launch_clip(const ClipArgs& a, hipStream_t stream);
 
-// ---- attention_fwd.hip, attention_bwd.hip ----
+// ---- attention_fwd.hip, attention_bwd.hip, attention_join.hip ----
 // A [batch, token, head, dim] tensor: element strides (the last one is 1).
 struct AttnView {
   uint16_t* p;
@@ -183,9 +183,29 @@ struct AttnArgs {
   int H, Hkv, D;
   float scale;
   bool causal;
+  // Workgroups that share one tile's walk over the other side.  With more
+  // than one, each leaves an fp32 partial result in `part` (forward: its
+  // normalized output, and its log-sum-exp in part_lse), which the join adds.
+  int splits;
+  int64_t all;                 // rows of all heads
+  float* part;                 // [splits][all][D]
+  float* part_lse;             // [splits][all]
 };
-hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
-hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t stream);
+enum AttnPass { kAttnFwd, kAttnDq, kAttnDkv };
+// How many workgroups share a tile in a pass (from the shapes alone).
+int attn_splits(const AttnArgs& a, AttnPass pass);
+// fp32 words of workspace: the forward's partial results; the backward
+// pass's delta and partial results.
+int64_t attn_fwd_workspace(const AttnArgs& a);
+int64_t attn_bwd_workspace(const AttnArgs& a);
+hipError_t launch_attn_fwd(const AttnArgs& a, float* ws, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnArgs& a, float* ws, hipStream_t stream);
+// Adds partial results: the forward's (weighted by their shares of the
+// softmax) into o and lse; n tensors' ([n][splits][rows][D]) into out[i]
+// times mul[i].
+hipError_t launch_attn_join_fwd(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_join_sum(const AttnArgs& a, int n, const AttnView* out, const float* mul,
+                                int64_t rows, int heads, hipStream_t stream);
 
 // ---- stream.hip: read-only HBM stream (measurement helper) ----
 // Reads bytes / 16 16-byte words of src with `grid` workgroups of 256

@@ -147,7 +147,8 @@ class _AttnCall:
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True,
                   scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
                   cu_seqlens_k: Optional[torch.Tensor] = None,
-                  out: Optional[torch.Tensor] = None, stream=None):
+                  out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                  stream=None):
     """softmax(scale q k^T) v per head, and the rows' log-sum-exp (fp32).
 
     Dense: q [B, Sq, H, D], k and v [B, Sk, Hkv, D]; returns out like q and
@@ -164,8 +165,12 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
         if out is None:
             out = torch.empty(c.q_shape, dtype=torch.bfloat16, device=c.dev)
         lse = torch.empty(c.lse_shape, dtype=torch.float32, device=c.dev)
-        check(lib().qlora_attention_fwd(c.c, c.q, c.k, c.v, c.heads("out", out), lse.data_ptr(),
-                                        st), "qlora_attention_fwd")
+        L = lib()
+        need = int(L.qlora_attention_fwd_workspace_size(c.c))
+        ws = _scratch(need, c.dev, ws) if need else None
+        check(L.qlora_attention_fwd(c.c, c.q, c.k, c.v, c.heads("out", out), lse.data_ptr(),
+                                    None if ws is None else ws.data_ptr(), _bytes(ws), st),
+              "qlora_attention_fwd")
     return out, lse
 
 

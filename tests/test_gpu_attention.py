@@ -132,6 +132,13 @@ DENSE = [
     (1, 511, 1025, 2, 2, 128, True),
     (1, 1025, 511, 2, 2, 64, False),
     (5, 97, 97, 7, 7, 120, True),
+    # walks that several workgroups share
+    (1, 1, 5000, 2, 1, 128, True),
+    (1, 40, 3001, 1, 1, 64, False),
+    (1, 3001, 40, 4, 1, 128, False),
+    (1, 3001, 40, 4, 1, 128, True),
+    (1, 1500, 1500, 4, 1, 128, True),
+    (2, 777, 1300, 2, 1, 40, True),
 ]
 
 
@@ -185,6 +192,7 @@ PACKED = [
     ([0, 0, 0], 2, 1, 64, True, 70),
     ([3] * 150, 1, 1, 64, True, 5),             # more sequences than lanes
     ([129, 257, 511], 5, 5, 80, True, 1),
+    ([900, 3, 1100], 4, 1, 128, True, 150),     # shared walks
 ]
 
 
@@ -272,6 +280,21 @@ def test_scale_and_another_stream():
         b = check_all(q, k, v, do, True, scale=0.5)
     for x, y in zip(a, b):   # and the same bits on every run
         assert torch.equal(x, y)
+
+
+def test_shared_walks_are_the_same_on_every_run():
+    say("[attention] shared walks, determinism")
+    q, do = draw(1, 1, 1000, 4, 64), draw(2, 1, 1000, 4, 64)
+    k, v = draw(3, 1, 1000, 1, 64), draw(4, 1, 1000, 1, 64)
+    c = qn.train_ops._AttnCall(q, k, v, True, None, None, None).c
+    assert qn.lib().qlora_attention_fwd_workspace_size(c) > 0
+    assert qn.lib().qlora_attention_bwd_workspace_size(c) > 4000 * 4
+    runs = []
+    for _ in range(2):
+        o, lse = qn.attention_fwd(q, k, v)
+        runs.append((o, lse, *qn.attention_bwd(q, k, v, o, lse, do)))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("lq,lk,n", [(0, 5, 1), (5, 0, 2), (0, 0, 1), (4, 4, 0)])

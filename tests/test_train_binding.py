@@ -152,7 +152,7 @@ def _view(**kw):
 
 def _fwd(a, q=None, k=None, v=None, o=None, lse=P):
     vs = [x if x is not None else _view() for x in (q, k, v, o)]
-    return _lib.lib().qlora_attention_fwd(a, *vs, lse, None)
+    return _lib.lib().qlora_attention_fwd(a, *vs, lse, P, 1 << 30, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -163,6 +163,7 @@ def _fwd(a, q=None, k=None, v=None, o=None, lse=P):
     dict(heads=1 << 30, q_rows=1000)], ids=str)
 def test_attention_abi_rejects_bad_sizes(bad):
     assert _fwd(_attn(**bad)) == INVALID
+    assert _lib.lib().qlora_attention_fwd_workspace_size(_attn(**bad)) == 0
     assert _lib.lib().qlora_attention_bwd_workspace_size(_attn(**bad)) == 0
 
 
@@ -198,7 +199,13 @@ def test_attention_abi_rejects_missing_statistics_and_small_workspaces():
         return L.qlora_attention_bwd(_attn(), *vs[:4], lse, *vs[4:], ws, nbytes, None)
     assert bwd(lse=None) == INVALID and bwd(ws=None) == INVALID and bwd(ws=P + 4) == INVALID
     assert bwd(nbytes=need - 1) == WORKSPACE
-    assert L.qlora_attention_fwd(None, *vs[:4], P, None) == INVALID
+    assert L.qlora_attention_fwd(None, *vs[:4], P, P, 0, None) == INVALID
+    few = _attn(n_seq=1, q_rows=1, k_rows=1 << 16)   # one query, many keys: split
+    need = L.qlora_attention_fwd_workspace_size(few)
+    assert need > 0
+    assert L.qlora_attention_fwd(few, *vs[:4], P, P, need - 1, None) == WORKSPACE
+    assert L.qlora_attention_fwd(few, *vs[:4], P, None, need, None) == INVALID
+    assert L.qlora_attention_fwd(few, *vs[:4], P, P + 8, need, None) == INVALID
 
 
 def test_attention_abi_with_no_queries_does_nothing():
