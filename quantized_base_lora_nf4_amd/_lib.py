@@ -188,7 +188,7 @@ def lib() -> ctypes.CDLL:
     L.qlora_config_error.argtypes = [vp, i64, i64, i32, i32, vp, vp, i32, vp, vp, sz, vp]
     L.qlora_ilp_plan.restype = i32
     L.qlora_ilp_plan.argtypes = [i32, i32, vp, vp, i64, vp, vp, vp]
-    pa, ph = ctypes.POINTER(Attention), ctypes.POINTER(Heads)
+    pa, ph = ctypes.POINTER(Attention), vp   # the tensors: addresses of qlora_heads_t
     L.qlora_attention_fwd.restype = i32
     L.qlora_attention_fwd.argtypes = [pa, ph, ph, ph, ph, vp, vp, sz, vp]
     L.qlora_attention_fwd_workspace_size.restype = sz

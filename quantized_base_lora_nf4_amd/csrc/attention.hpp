@@ -80,12 +80,17 @@ __device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
 }
 
 // Dense: every sequence has the same tiles, ntiles = ceil(cols / kBlock).
-// Packed: `slots` tiles per head, at least as many as all sequences have;
-// the tile's sequence is found from the lengths (64 at a time, by a prefix
-// sum over the wave).  After the last sequence, the rows that belong to
-// none form one more, with nothing on the other side, so that outputs are
-// zero there.  Offsets are clamped to the tensors' rows, so that wrong
-// ones give wrong results but no access out of range.
+// Packed: `slots` tiles per head, at least as many as all sequences have.
+// Up to 63 sequences, the tiles are taken by the length of their walk, the
+// longest first: with a causal mask a sequence of n tiles has one of each
+// length 1 .. n, so the tiles of one length are found by a ballot over the
+// sequences; without one, all its tiles have length n.  With more sequences
+// the tiles are taken sequence by sequence (64 lengths at a time, by a prefix
+// sum over the wave).
+// After the last sequence, the rows that belong to none form one more, with
+// nothing on the other side, so that outputs are zero there.  Offsets are
+// clamped to the tensors' rows, so that wrong ones give wrong results but no
+// access out of range.
 // kKeys: the columns are keys (the dK/dV kernel), else queries.
 template <bool kKeys>
 __device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned heads) {
@@ -113,39 +118,65 @@ __device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned
   const int lane = threadIdx.x & 63;
   const int32_t* cu = kKeys ? p.cu_k : p.cu_q;
   const int64_t rows = kKeys ? p.Sk : p.Sq;
-  int base = 0;
-  for (int s0 = 0; s0 <= p.nseq; s0 += 64) {
-    const int s = s0 + lane;
-    int n = 0;
-    if (s <= p.nseq) {
-      const int64_t a = clamp_row(cu[s], 0, rows);
-      const int64_t b = s < p.nseq ? clamp_row(cu[s + 1], a, rows) : rows;
-      n = (int)((b - a + kBlock - 1) / kBlock);
-    }
-    int sum = n;
+  int found = -1, tile = 0, n = 0;  // sequence, and in its lane: tiles
+  auto tiles_of = [&](int s) {
+    if (s > p.nseq) return 0;
+    const int64_t a = clamp_row(cu[s], 0, rows);
+    const int64_t b = s < p.nseq ? clamp_row(cu[s + 1], a, rows) : rows;
+    return (int)((b - a + kBlock - 1) / kBlock);
+  };
+  if (p.nseq < 64) {
+    n = tiles_of(lane);
+    int longest = n;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += up;
+    for (int o = 32; o > 0; o >>= 1) {
+      const int other = __shfl_xor(longest, o, 64);
+      longest = longest > other ? longest : other;
     }
-    const uint64_t past = __ballot(base + sum > slot);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      const int sq = __builtin_amdgcn_readfirstlane(s0 + l);
-      w.ntiles = __builtin_amdgcn_readfirstlane(__shfl(n, l, 64));
-      w.tile = slot - base - __builtin_amdgcn_readfirstlane(__shfl(sum - n, l, 64));
-      const bool none = sq == p.nseq;
-      w.q0 = clamp_row(p.cu_q[sq], 0, p.Sq);
-      w.k0 = clamp_row(p.cu_k[sq], 0, p.Sk);
-      const int qe = none ? (kKeys ? (int)w.q0 : (int)p.Sq) : clamp_row(p.cu_q[sq + 1], w.q0, p.Sq);
-      const int ke = none ? (kKeys ? (int)p.Sk : (int)w.k0) : clamp_row(p.cu_k[sq + 1], w.k0, p.Sk);
-      w.lq = qe - (int)w.q0;
-      w.lk = ke - (int)w.k0;
-      w.valid = true;
-      return w;
+    int left = slot;
+    for (int len = __builtin_amdgcn_readfirstlane(longest); len > 0; --len) {
+      uint64_t has = __ballot(p.causal ? n >= len : n == len);
+      const int each = p.causal ? 1 : len, count = __popcll(has) * each;
+      if (left < count) {
+        for (int i = left / each; i > 0; --i) has &= has - 1;
+        found = __ffsll((unsigned long long)has) - 1;
+        w.ntiles = __builtin_amdgcn_readlane(n, found);
+        tile = p.causal ? w.ntiles - len : left % each;
+        break;
+      }
+      left -= count;
     }
-    base += __builtin_amdgcn_readlane(sum, 63);
+  } else {
+    int base = 0;
+    for (int s0 = 0; s0 <= p.nseq; s0 += 64) {
+      n = tiles_of(s0 + lane);
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += up;
+      }
+      const uint64_t past = __ballot(base + sum > slot);
+      if (past) {
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+        found = s0 + l;
+        w.ntiles = __builtin_amdgcn_readlane(n, l);
+        tile = slot - base - __builtin_amdgcn_readlane(sum - n, l);
+        break;
+      }
+      base += __builtin_amdgcn_readlane(sum, 63);
+    }
   }
+  if (found < 0) return w;
+  const bool none = found == p.nseq;
+  w.tile = tile;
+  w.q0 = clamp_row(p.cu_q[found], 0, p.Sq);
+  w.k0 = clamp_row(p.cu_k[found], 0, p.Sk);
+  const int qe = none ? (kKeys ? (int)w.q0 : (int)p.Sq) : clamp_row(p.cu_q[found + 1], w.q0, p.Sq);
+  const int ke = none ? (kKeys ? (int)p.Sk : (int)w.k0) : clamp_row(p.cu_k[found + 1], w.k0, p.Sk);
+  w.lq = qe - (int)w.q0;
+  w.lk = ke - (int)w.k0;
+  w.valid = true;
   return w;
 }
 

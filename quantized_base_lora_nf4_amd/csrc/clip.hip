@@ -20,7 +20,8 @@
 namespace qn {
 namespace {
 
-constexpr int64_t kChunk = 16384;  // elements per unit of work
+constexpr int64_t kChunk = 10240;  // elements per unit of work: 20 KB of bf16, 40 KB of fp32
+constexpr int kUnroll = 5;         // vectors in flight per thread; a chunk is 5 or 10 per thread
 constexpr int kNT = 256;
 
 struct NormTable {
@@ -99,17 +100,17 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
 }
 
 template <class E>
-__device__ __forceinline__ void chunk_squares(double (&a)[4], const E* p, int count, bool f32) {
+__device__ __forceinline__ void chunk_squares(double (&a)[kUnroll], const E* p, int count, bool f32) {
   constexpr int VEC = 16 / (int)sizeof(E);
   const int nv = count / VEC;
   int i = threadIdx.x;
-  for (; i + 3 * kNT < nv; i += 4 * kNT) {
-    u32x4 v[4];
+  for (; i + (kUnroll - 1) * kNT < nv; i += kUnroll * kNT) {
+    u32x4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kUnroll; ++u)
       v[u] = reinterpret_cast<const Loose16<E>*>(p + (int64_t)(i + u * kNT) * VEC)->v;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) add_squares(a[u], v[u], f32);
+    for (int u = 0; u < kUnroll; ++u) add_squares(a[u], v[u], f32);
   }
   for (; i < nv; i += kNT)
     add_squares(a[0], reinterpret_cast<const Loose16<E>*>(p + (int64_t)i * VEC)->v, f32);
@@ -124,12 +125,15 @@ __device__ __forceinline__ void chunk_squares(double (&a)[4], const E* p, int co
 
 __global__ __launch_bounds__(kNT) void k_grad_squares(NormTable tb, double* __restrict__ part) {
   __shared__ double s[kNT / 64];
-  double a[4] = {0.0, 0.0, 0.0, 0.0};
+  double a[kUnroll] = {};
   for_chunks(tb, [&](int t, int64_t first, int count, bool f32) {
     if (f32) chunk_squares(a, (const float*)tb.g[t] + first, count, true);
     else chunk_squares(a, (const uint16_t*)tb.g[t] + first, count, false);
   });
-  const double v = block_sum((a[0] + a[1]) + (a[2] + a[3]), s);
+  double sum = 0.0;
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) sum += a[u];
+  const double v = block_sum(sum, s);
   if (threadIdx.x == 0) part[blockIdx.x] = v;
 }
 
@@ -155,15 +159,19 @@ __device__ __forceinline__ void chunk_scale(E* out, const E* p, int count, float
   constexpr bool f32 = sizeof(E) == 4;
   const int nv = count / VEC;
   int i = threadIdx.x;
-  for (; i + 3 * kNT < nv; i += 4 * kNT) {
-    u32x4 v[4];
+  for (; i + (kUnroll - 1) * kNT < nv; i += kUnroll * kNT) {
+    u32x4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kUnroll; ++u)
       v[u] = reinterpret_cast<const Loose16<E>*>(p + (int64_t)(i + u * kNT) * VEC)->v;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      reinterpret_cast<Loose16<E>*>(out + (int64_t)(i + u * kNT) * VEC)->v =
-          scale_vec(v[u], c, f32);
+    for (int u = 0; u < kUnroll; ++u)
+      // Nontemporal: written through instead of left dirty in the Infinity
+      // Cache, whose write-back would share HBM with the next pass's reads
+      // (448 tensors, 320 MB: 198 -> 185 us for the whole call).
+      __builtin_nontemporal_store(
+          scale_vec(v[u], c, f32),
+          &reinterpret_cast<Loose16<E>*>(out + (int64_t)(i + u * kNT) * VEC)->v);
   }
   for (; i < nv; i += kNT)
     reinterpret_cast<Loose16<E>*>(out + (int64_t)i * VEC)->v =
@@ -199,14 +207,15 @@ __global__ __launch_bounds__(kNT) void k_grad_norm(const double* __restrict__ pa
   if (threadIdx.x == 0) *norm_out = (float)norm;
 }
 
-// Fills a launch's table from tensor i on (empty tensors are left out) and
-// returns the first tensor that is not in it.
+// Fills a launch's table with the tensors from i on towards n (upwards or
+// downwards; empty ones are left out) and returns the first that is not in it.
 template <class Table, class Add>
 int64_t fill(Table& tb, int cap, int64_t i, int64_t n, const int64_t* sizes, const int32_t* types,
              Add&& add) {
   uint32_t end = 0;
   tb.n = 0;
-  for (; i < n && tb.n < cap; ++i) {
+  const int64_t dir = n < i ? -1 : 1;
+  for (; i != n && tb.n < cap; i += dir) {
     if (sizes[i] == 0) continue;
     const int64_t chunks = (sizes[i] + kChunk - 1) / kChunk;
     if (end + (uint64_t)chunks > 0x7fffffffu) break;  // the next launch takes it
@@ -240,10 +249,12 @@ hipError_t launch_clip(const ClipArgs& a, hipStream_t stream) {
   }
   float* norm_out = a.norm;
   if (a.scale) {
-    for (int64_t i = 0; i < a.n;) {
+    // From the last tensor to the first: what the sum read last is still in the
+    // 256 MB Infinity Cache.
+    for (int64_t i = a.n - 1; i >= 0;) {
       ScaleTable tb;
       bool in_place = true;
-      i = fill(tb, kClipScaleTable, i, a.n, a.sizes, a.types, [&](int k, int64_t t) {
+      i = fill(tb, kClipScaleTable, i, -1, a.sizes, a.types, [&](int k, int64_t t) {
         tb.g[k] = a.grads[t];
         tb.out[k] = a.out ? a.out[t] : const_cast<void*>(a.grads[t]);
         in_place = in_place && tb.out[k] == tb.g[k];

@@ -217,100 +217,115 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm_fwd(
   }
 }
 
-// Backward: workgroup `blockIdx.x` of G takes rows blockIdx.x, + G, ...; a
-// thread owns the same columns of every row, so its share of dw and db adds
-// up in registers, and each workgroup writes one row of partial sums
-// part[2][G][width] (dw, then db if kBias).  k_norm_bwd_params adds the
-// G partial rows in a fixed order.
-template <class T, class PT, int TPR, int NV, bool kRms, bool kBias>
-__global__ __launch_bounds__(TPR) void k_norm_bwd(
+// Backward: a workgroup holds RG = NT / TPR row groups of TPR threads.  Group
+// k of workgroup b takes rows b RG + k, + gridDim.x RG, ...; a thread owns the
+// same columns of every row, so its share of dw and db adds up in registers.
+// At the end the groups' shares are added pairwise through LDS, and the
+// workgroup writes one row of partial sums part[2][G][width] (dw, then db if
+// kBias), which k_norm_bwd_params adds in a fixed order.  The next row's loads
+// run during the current one.
+//
+// Few, large workgroups keep the partial rows few: at 256 of them their
+// traffic is 2 % of the pass at 8192 x 8192 and 12 % at 4096 x 1024 (bf16).
+template <class T, class PT, int NT, int TPR, int NV, bool kRms, bool kBias>
+__global__ __launch_bounds__(NT) void k_norm_bwd(
     const typename T::elem* __restrict__ dy, const typename T::elem* __restrict__ x, int64_t rows,
     int width, const typename PT::elem* __restrict__ w, const float* __restrict__ mean,
     const float* __restrict__ rstd, typename T::elem* __restrict__ dx, float* __restrict__ part) {
-  constexpr int VEC = T::VEC;
-  __shared__ float red[TPR > 64 ? 4 * TPR / 64 : 1];
-  const int t = threadIdx.x;
+  constexpr int VEC = T::VEC, RG = NT / TPR, W = TPR / 64;
+  constexpr int kSums = W > 1 ? 4 * (NT / 64) : 1;            // floats for the row sums
+  constexpr int kShare = RG > 1 ? RG / 2 * TPR * NV * VEC : 1;  // and for half of the groups' shares
+  __shared__ __attribute__((aligned(16))) float red[kSums];
+  __shared__ __attribute__((aligned(16))) float share[kShare];
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const float inv_n = 1.0f / (float)width;
-  float aw[NV][VEC], ab[kBias ? NV : 1][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      aw[i][e] = 0.0f;
-      if constexpr (kBias) ab[i][e] = 0.0f;
-    }
+  // Up to two vectors per thread, the weight stays in registers and the next
+  // row is fetched ahead; with more there are not enough of them.
+  constexpr bool kHold = NV <= 2;
+  float aw[NV][VEC] = {}, ab[kBias ? NV : 1][VEC] = {};
   float wv[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
+  auto load_w = [&](int i) {
     const int col = (i * TPR + t) * VEC;
     load_params<PT, VEC>(wv[i], w, col < width ? col : 0, col < width ? width : 0);
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load_w(i);
   }
   int flip = 0;
   u32x4 nx[NV], ny[NV];
   float nmu = 0.0f, nrs = 0.0f;
+  // A row past the end has dy = 0 and adds nothing.
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * VEC;
-      const bool in = col < width;
+      const bool in = col < width && row < rows;
       nx[i] = in ? load_vec<T>(x + row * width, col, width) : u32x4{0u, 0u, 0u, 0u};
       ny[i] = in ? load_vec<T>(dy + row * width, col, width) : u32x4{0u, 0u, 0u, 0u};
     }
-    if constexpr (!kRms) nmu = mean[row];
-    nrs = rstd[row];
+    nmu = !kRms && row < rows ? mean[row] : 0.0f;
+    nrs = row < rows ? rstd[row] : 0.0f;
   };
-  int64_t row = blockIdx.x;
-  if (row < rows) fetch(row);
-  for (; row < rows; row += gridDim.x) {
+  const int64_t stride = (int64_t)gridDim.x * RG;
+  int64_t row = (int64_t)blockIdx.x * RG + group;
+  if constexpr (kHold) fetch(row);
+  // the same number of turns in every group: there is a barrier in each
+  for (int64_t base = (int64_t)blockIdx.x * RG; base < rows; base += stride, row += stride) {
     u32x4 vx[NV], vy[NV];
+    if constexpr (!kHold) fetch(row);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       vx[i] = nx[i];
       vy[i] = ny[i];
     }
     const float mu = nmu, rs = nrs;
-    if (row + gridDim.x < rows) fetch(row + gridDim.x);  // the next row, in flight meanwhile
+    if constexpr (kHold) {
+      if (base + stride < rows) fetch(row + stride);
+    }
     float sg = 0.0f, sz = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (!kHold) load_w(i);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         // past the width: dy = 0 and w = 0, so nothing is added
         const float z = (vec_get<T>(vx[i], e) - mu) * rs;
         const float d = vec_get<T>(vy[i], e);
         const float g = d * wv[i][e];
-        sg += g;
+        if constexpr (!kRms) sg += g;
         sz += g * z;
         aw[i][e] += d * z;
         if constexpr (kBias) ab[i][e] += d;
       }
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
       sz += __shfl_xor(sz, o, 64);
       if constexpr (!kRms) sg += __shfl_xor(sg, o, 64);
     }
-    if constexpr (TPR > 64) {
-      constexpr int W = TPR / 64;
-      float* r = red + flip * 2 * W;
+    if constexpr (W > 1) {
+      float* r = red + flip * 2 * (NT / 64);
       flip ^= 1;
-      if ((t & 63) == 0) {
-        r[2 * (t >> 6)] = sz;
-        r[2 * (t >> 6) + 1] = sg;
+      if ((threadIdx.x & 63) == 0) {
+        r[2 * (threadIdx.x >> 6)] = sz;
+        r[2 * (threadIdx.x >> 6) + 1] = sg;
       }
       __syncthreads();
       sz = sg = 0.0f;
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        sz += r[2 * k];
-        sg += r[2 * k + 1];
+        sz += r[2 * (group * W + k)];
+        if constexpr (!kRms) sg += r[2 * (group * W + k) + 1];
       }
     }
     const float cz = sz * inv_n, cg = kRms ? 0.0f : sg * inv_n;
-    if (dx) {
+    if (dx && row < rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + t) * VEC;
         if (col < width) {
+          if constexpr (!kHold) load_w(i);
           float f[VEC];
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
@@ -323,6 +338,39 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(
     }
   }
   if (!part) return;
+  // upper half of the groups -> LDS -> lower half, until one group has it all
+  auto gather = [&](float (&a)[NV][VEC]) {
+#pragma unroll
+    for (int half = RG / 2; half > 0; half /= 2) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int h = 0; h < VEC; h += 4) {
+          f32x4* p = reinterpret_cast<f32x4*>(
+              share + ((((group & (half - 1)) * NV + i) * (VEC / 4) + h / 4) * TPR + t) * 4);
+          if (group >= half && group < 2 * half)
+            *p = f32x4{a[i][h], a[i][h + 1], a[i][h + 2], a[i][h + 3]};
+        }
+      __syncthreads();
+      if (group < half) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int h = 0; h < VEC; h += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(
+                share + (((group * NV + i) * (VEC / 4) + h / 4) * TPR + t) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[i][h + e] += v[e];
+          }
+      }
+    }
+  };
+  if constexpr (RG > 1) {
+    gather(aw);
+    if constexpr (kBias) gather(ab);
+    if (group > 0) return;
+  }
   float* pw = part + (int64_t)blockIdx.x * width;
   float* pb = pw + (int64_t)gridDim.x * width;
 #pragma unroll
@@ -339,8 +387,10 @@ __global__ __launch_bounds__(TPR) void k_norm_bwd(
 }
 
 // dw (and db) from the G partial rows: 64 columns per workgroup of 16
-// waves, each wave adding every 16th row; then the 16 sums in wave order.
+// waves, each wave adding every 16th row (at most 16 of them, all loaded at
+// once); then the 16 sums in wave order.
 constexpr int kPW = 16;
+constexpr int kMaxGroups = 256;  // one workgroup per CU
 template <class PT>
 __global__ __launch_bounds__(64 * kPW) void k_norm_bwd_params(const float* __restrict__ part,
                                                               int G, int width,
@@ -353,15 +403,14 @@ __global__ __launch_bounds__(64 * kPW) void k_norm_bwd_params(const float* __res
   const float* p = part + (blockIdx.y ? (int64_t)G * width : 0);
   float a = 0.0f;
   if (col < width) {
-    int g = wave;
-    for (; g + 3 * kPW < G; g += 4 * kPW) {
-      float v[4];
+    float v[kMaxGroups / kPW];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = p[(int64_t)(g + u * kPW) * width + col];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) a += v[u];
+    for (int u = 0; u < kMaxGroups / kPW; ++u) {
+      const int g = wave + u * kPW;
+      v[u] = g < G ? p[(int64_t)g * width + col] : 0.0f;
     }
-    for (; g < G; g += kPW) a += p[(int64_t)g * width + col];
+#pragma unroll
+    for (int u = 0; u < kMaxGroups / kPW; ++u) a += v[u];
   }
   s[wave][lane] = a;
   __syncthreads();
@@ -390,15 +439,17 @@ template <int V>
 using IntC = std::integral_constant<int, V>;
 
 // Forward: threads per row and vectors per thread.  A wave per row has no
-// barriers and is taken while there are rows enough to fill the chip;
-// otherwise a row is spread over more threads.
+// barriers and is taken for up to 256 vectors while there are rows enough to
+// fill the chip (16384 x 1024 bf16: 14.1 us against 21.9 with 256 threads);
+// with more vectors a wave's row takes the registers that would keep more
+// loads in flight (4096 x 4096 bf16: 20.1 us against 14.6), and with few rows
+// one wave's latency counts: there a row is spread over more threads.
 template <class F>
 hipError_t with_fwd_shape(int64_t rows, int64_t nv, F&& f) {
   const bool many = rows >= 2048;
   if (nv <= 64) return f(IntC<64>{}, IntC<1>{});
   if (nv <= 128 && many) return f(IntC<64>{}, IntC<2>{});
   if (nv <= 256 && many) return f(IntC<64>{}, IntC<4>{});
-  if (nv <= 512 && many) return f(IntC<64>{}, IntC<8>{});
   if (nv <= 256) return f(IntC<256>{}, IntC<1>{});
   if (nv <= 512) return f(IntC<256>{}, IntC<2>{});
   if (nv <= 1024) return f(IntC<256>{}, IntC<4>{});
@@ -407,18 +458,25 @@ hipError_t with_fwd_shape(int64_t rows, int64_t nv, F&& f) {
   return f(IntC<1024>{}, IntC<8>{});
 }
 
-// Backward: as many threads as cover the row with one vector each, up to
-// 512; wider rows take several vectors per thread.
+// Backward: threads per workgroup and row, and vectors per thread: a wave per
+// row up to two vectors per lane (no barriers), otherwise as many threads as
+// give each one vector.  Sums of dw and db take 16 registers per bf16 vector
+// and 8 per fp32 vector, and 1024 threads have 128 each, 512 threads 256:
+// two or more bf16 vectors per thread run faster in the smaller workgroup
+// (16384 x 1024: 32.9 -> 21.5 us; 2000 x 16384: 62 -> 49 us), two fp32
+// vectors in the larger one (2048 x 5120: 24.4 us against 28.0).
 template <class F>
-auto with_bwd_shape(int64_t nv, F&& f) {
-  if (nv <= 64) return f(IntC<64>{}, IntC<1>{});
-  if (nv <= 128) return f(IntC<128>{}, IntC<1>{});
-  if (nv <= 256) return f(IntC<256>{}, IntC<1>{});
-  if (nv <= 512) return f(IntC<512>{}, IntC<1>{});
-  if (nv <= 1024) return f(IntC<512>{}, IntC<2>{});
-  if (nv <= 2048) return f(IntC<512>{}, IntC<4>{});
-  if (nv <= 4096) return f(IntC<1024>{}, IntC<4>{});
-  return f(IntC<1024>{}, IntC<8>{});
+auto with_bwd_shape(int64_t nv, int type, F&& f) {
+  if (nv <= 64) return f(IntC<1024>{}, IntC<64>{}, IntC<1>{});
+  if (nv <= 128) return f(IntC<512>{}, IntC<64>{}, IntC<2>{});
+  if (nv <= 256) return f(IntC<1024>{}, IntC<256>{}, IntC<1>{});
+  if (nv <= 512) return f(IntC<1024>{}, IntC<512>{}, IntC<1>{});
+  if (nv <= 1024) return f(IntC<1024>{}, IntC<1024>{}, IntC<1>{});
+  if (nv <= 2048)
+    return type == kNormF32 ? f(IntC<1024>{}, IntC<1024>{}, IntC<2>{})
+                            : f(IntC<512>{}, IntC<512>{}, IntC<4>{});
+  if (nv <= 4096) return f(IntC<1024>{}, IntC<1024>{}, IntC<4>{});
+  return f(IntC<1024>{}, IntC<1024>{}, IntC<8>{});
 }
 
 }  // namespace
@@ -428,10 +486,11 @@ int64_t norm_max_width(int type) {
 }
 
 int norm_bwd_groups(int64_t rows, int64_t width, int type) {
-  const int tpr = with_bwd_shape(row_vecs(width, type),
-                                 [](auto tp, auto) { return (int)decltype(tp)::value; });
-  const int64_t g = 256 * 1024 / tpr;  // about 16 waves per CU
-  return (int)(rows < g ? rows : g);
+  const int rg = with_bwd_shape(row_vecs(width, type), type, [](auto nt, auto tp, auto) {
+    return (int)decltype(nt)::value / (int)decltype(tp)::value;
+  });
+  const int64_t g = (rows + rg - 1) / rg;
+  return (int)(g < kMaxGroups ? g : kMaxGroups);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
@@ -464,22 +523,23 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   if (G > 0) {
     const hipError_t e = with_norm_type(a.x_type, [&](auto t) {
       return with_norm_type(a.w_type, [&](auto pt) {
-        return with_bwd_shape(row_vecs(a.width, a.x_type), [&](auto tp, auto nv) {
+        return with_bwd_shape(row_vecs(a.width, a.x_type), a.x_type, [&](auto nt, auto tp, auto nv) {
           using T = decltype(t);
           using PT = decltype(pt);
-          constexpr int TPR = decltype(tp)::value, NV = decltype(nv)::value;
+          constexpr int NT = decltype(nt)::value, TPR = decltype(tp)::value,
+                        NV = decltype(nv)::value;
           auto go = [&](auto kern) {
-            kern<<<G, TPR, 0, stream>>>((const typename T::elem*)a.dy,
+            kern<<<G, NT, 0, stream>>>((const typename T::elem*)a.dy,
                                         (const typename T::elem*)a.x, a.rows, (int)a.width,
                                         (const typename PT::elem*)a.w, a.mean, a.rstd,
                                         (typename T::elem*)a.dx, a.dw || a.db ? a.part : nullptr);
             return hipGetLastError();
           };
           if (a.rms)
-            return a.db ? go(k_norm_bwd<T, PT, TPR, NV, true, true>)
-                        : go(k_norm_bwd<T, PT, TPR, NV, true, false>);
-          return a.db ? go(k_norm_bwd<T, PT, TPR, NV, false, true>)
-                      : go(k_norm_bwd<T, PT, TPR, NV, false, false>);
+            return a.db ? go(k_norm_bwd<T, PT, NT, TPR, NV, true, true>)
+                        : go(k_norm_bwd<T, PT, NT, TPR, NV, true, false>);
+          return a.db ? go(k_norm_bwd<T, PT, NT, TPR, NV, false, true>)
+                      : go(k_norm_bwd<T, PT, NT, TPR, NV, false, false>);
         });
       });
     });

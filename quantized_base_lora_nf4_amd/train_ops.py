@@ -9,13 +9,14 @@ that stream, and all arithmetic happens in the HIP kernels.
 
 import array
 import contextlib
-import ctypes
+import itertools
 import math
+import operator
 from typing import Optional
 
 import torch
 
-from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Heads, check, lib
+from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, check, lib
 from .ops import _stream_obj
 
 _SIXTEEN = (torch.bfloat16, torch.int16, torch.uint16)
@@ -26,10 +27,10 @@ _HERE = contextlib.nullcontext()
 def _on(device: torch.device, stream):
     """(stream handle, context to allocate and launch in) for tensors on
     `device`: the given stream, or the device's current one."""
-    other = device.index is not None and device.index != torch.cuda.current_device()
     if stream is None:
-        return (torch.cuda.current_stream(device).cuda_stream,
-                torch.cuda.device(device) if other else _HERE)
+        i = device.index
+        return (torch._C._cuda_getCurrentRawStream(i),
+                _HERE if i == torch.cuda.current_device() else torch.cuda.device(device))
     st = _stream_obj(stream)
     return st.cuda_stream, torch.cuda.stream(st)
 
@@ -44,6 +45,9 @@ def _device_of(name: str, t: torch.Tensor) -> torch.device:
 
 def _same(name: str, t, shape, dtypes, device) -> None:
     """Shape, dtype, device and layout of one contiguous tensor."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and
+            t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if tuple(t.shape) != tuple(shape):
@@ -60,6 +64,11 @@ def _bytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _new_like(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialized contiguous bf16 tensor of t's shape."""
+    return torch.empty_like(t, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+
+
 def _scratch(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
     if ws is not None:
         if ws.device != device or not ws.is_contiguous():
@@ -73,32 +82,9 @@ def _scratch(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
 # Attention
 # ---------------------------------------------------------------------------
 
-def _heads(name: str, t: torch.Tensor, shape, device, packed: bool) -> Heads:
-    """One [batch, row, head, dim] (packed: [row, head, dim]) tensor of any
-    strides that the kernels take."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in _SIXTEEN:
-        raise TypeError(f"{name} must be bf16 (or its 16-bit view), got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    st = t.stride()
-    if t.numel() == 0:
-        return Heads(None, 0, 0, 0)
-    # the stride of a dimension of size 1 says nothing
-    st = [0 if n == 1 else s for n, s in zip(shape, st[:-1])] + [st[-1]]
-    if (st[-1] != 1 and shape[-1] != 1) or any(s % 8 for s in st[:-1]):
-        raise ValueError(f"{name} needs contiguous head vectors and strides of a multiple of 8, "
-                         f"has {tuple(t.stride())}")
-    if packed:
-        return Heads(t.data_ptr(), 0, st[0], st[1])
-    return Heads(t.data_ptr(), st[0], st[1], st[2])
-
-
 class _AttnCall:
-    """Checked shapes of an attention call."""
+    """Checked arguments of an attention call.  Its tensors' (address, batch,
+    row and head stride) lie one after the other in `words`, as qlora_heads_t."""
 
     def __init__(self, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
         dev = _device_of("q", q)
@@ -110,18 +96,19 @@ class _AttnCall:
             if not isinstance(t, torch.Tensor) or t.dim() != nd:
                 raise ValueError(f"{name} must have {nd} dimensions "
                                  f"({'[row, head, dim]' if self.packed else '[batch, row, head, dim]'})")
-        h, d = q.shape[-2:]
-        hk = k.shape[-2]
+        self.dev = dev
+        self.q_shape = qs = q.shape
+        ks = k.shape
+        h, d = qs[-2], qs[-1]
+        hk = ks[-2]
         if h < 1 or hk < 1 or h % hk:
             raise ValueError(f"{h} query heads cannot share {hk} key/value heads")
-        self.dev = dev
-        self.q_shape = tuple(q.shape)
-        self.k_shape = ((k.shape[0],) if self.packed else (q.shape[0], k.shape[1])) + (hk, d)
         cq = ck = None
         if self.packed:
+            self.k_shape = (ks[0], hk, d)
             if cu_seqlens_k is None:
                 cu_seqlens_k = cu_seqlens
-                if k.shape[0] != q.shape[0]:
+                if ks[0] != qs[0]:
                     raise ValueError("q and k have different rows: cu_seqlens_k is needed")
             for name, c in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_seqlens_k)):
                 if not isinstance(c, torch.Tensor) or c.dim() != 1 or c.numel() < 1:
@@ -129,19 +116,47 @@ class _AttnCall:
                 _same(name, c, cu_seqlens.shape, (torch.int32,), dev)
             cq, ck = cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr()
             n = cu_seqlens.numel() - 1
-            self.lse_shape = (h, q.shape[0])
+            self.lse_shape = (h, qs[0])
         else:
-            n = q.shape[0]
-            self.lse_shape = (n, h, q.shape[1])
+            n = qs[0]
+            self.k_shape = (n, ks[1], hk, d)
+            self.lse_shape = (n, h, qs[1])
         if scale is None:
             scale = 1.0 / math.sqrt(d) if d else 1.0
-        self.c = Attention(n, self.q_shape[-3], self.k_shape[-3], cq, ck, h, hk, d, int(causal),
-                           float(scale))
-        self.q, self.k, self.v = self.heads("q", q), self.heads("k", k), self.heads("v", v)
+        self.c = Attention(n, qs[-3], ks[-3], cq, ck, h, hk, d, int(causal), float(scale))
+        self.words = []
+        self.add("q", q, self.q_shape)
+        self.add("k", k, self.k_shape)
+        self.add("v", v, self.k_shape)
 
-    def heads(self, name, t):
-        shape = self.k_shape if name in ("k", "v", "dk", "dv") else self.q_shape
-        return _heads(name, t, shape, self.dev, self.packed)
+    def add(self, name, t, shape) -> None:
+        """One more [batch, row, head, dim] (packed: [row, head, dim]) tensor,
+        of any strides that the kernels take."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype not in _SIXTEEN:
+            raise TypeError(f"{name} must be bf16 (or its 16-bit view), got {t.dtype}")
+        if t.device != self.dev:
+            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
+        if t.numel() == 0:
+            self.words += (0, 0, 0, 0)
+            return
+        st = t.stride()
+        if st[-1] != 1 or (st[-2] | st[-3] | st[0]) & 7:
+            # the stride of a dimension of size 1 says nothing
+            st = [0 if n == 1 else s for n, s in zip(shape, st[:-1])] + [st[-1]]
+            if (st[-1] != 1 and shape[-1] != 1) or any(s % 8 for s in st[:-1]):
+                raise ValueError(f"{name} needs contiguous head vectors and strides of a multiple "
+                                 f"of 8, has {t.stride()}")
+        self.words += (t.data_ptr(), 0 if self.packed else st[0], st[-3], st[-2])
+
+    def views(self):
+        """The addresses of the tensors' descriptions, in the order added."""
+        self.array = array.array("q", self.words)
+        base = self.array.buffer_info()[0]
+        return range(base, base + 8 * len(self.words), 32)
 
 
 def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True,
@@ -163,12 +178,13 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
     st, ctx = _on(c.dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty(c.q_shape, dtype=torch.bfloat16, device=c.dev)
+            out = _new_like(q)
         lse = torch.empty(c.lse_shape, dtype=torch.float32, device=c.dev)
         L = lib()
         need = int(L.qlora_attention_fwd_workspace_size(c.c))
         ws = _scratch(need, c.dev, ws) if need else None
-        check(L.qlora_attention_fwd(c.c, c.q, c.k, c.v, c.heads("out", out), lse.data_ptr(),
+        c.add("out", out, c.q_shape)
+        check(L.qlora_attention_fwd(c.c, *c.views(), lse.data_ptr(),
                                     None if ws is None else ws.data_ptr(), _bytes(ws), st),
               "qlora_attention_fwd")
     return out, lse
@@ -184,19 +200,21 @@ def attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Te
     three tensors to write."""
     c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     _same("lse", lse, c.lse_shape, (torch.float32,), c.dev)
-    oh, gh = c.heads("o", o), c.heads("do", do)
+    c.add("o", o, c.q_shape)
+    c.add("do", do, c.q_shape)
     st, ctx = _on(c.dev, stream)
     with ctx:
         if out is None:
-            out = (torch.empty(c.q_shape, dtype=torch.bfloat16, device=c.dev),
-                   torch.empty(c.k_shape, dtype=torch.bfloat16, device=c.dev),
-                   torch.empty(c.k_shape, dtype=torch.bfloat16, device=c.dev))
+            out = _new_like(q), _new_like(k), _new_like(k)
         dq, dk, dv = out
         L = lib()
         ws = _scratch(int(L.qlora_attention_bwd_workspace_size(c.c)), c.dev, ws)
-        check(L.qlora_attention_bwd(c.c, c.q, c.k, c.v, oh, lse.data_ptr(), gh,
-                                    c.heads("dq", dq), c.heads("dk", dk), c.heads("dv", dv),
-                                    ws.data_ptr(), _bytes(ws), st), "qlora_attention_bwd")
+        c.add("dq", dq, c.q_shape)
+        c.add("dk", dk, c.k_shape)
+        c.add("dv", dv, c.k_shape)
+        v = c.views()
+        check(L.qlora_attention_bwd(c.c, *v[:4], lse.data_ptr(), *v[4:], ws.data_ptr(),
+                                    _bytes(ws), st), "qlora_attention_bwd")
     return dq, dk, dv
 
 
@@ -357,26 +375,32 @@ class RMSNorm(torch.nn.Module):
 # Gradient norm and clipping
 # ---------------------------------------------------------------------------
 
-def _addresses(values) -> "array.array":
-    return array.array("Q", values)
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _grad_arrays(name: str, grads):
-    """(device, sizes, types) of a list of gradients, after one look at each."""
+    """(device, addresses, sizes, types) of a list of gradients."""
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError(f"{name} must all be torch tensors")
     dev = _device_of(f"{name}[0]", grads[0])
-    kinds = {(t.dtype, t.device, t.is_contiguous()) for t in grads}
-    for dt, d, contiguous in kinds:
+    try:
+        devices = set(map(torch.Tensor.get_device, grads))
+    except TypeError:
+        raise TypeError(f"{name} must all be torch tensors") from None
+    if devices != {dev.index}:
+        other = max(devices - {dev.index})
+        raise ValueError(f"{name} are on {dev} and {f'cuda:{other}' if other >= 0 else 'cpu'}, "
+                         "expected one GPU")
+    dtypes = set(map(_dtype_of, grads))
+    for dt in dtypes:
         if dt not in _TYPES:
             raise TypeError(f"{name} must be bfloat16 or float32, one is {dt}")
-        if d != dev:
-            raise ValueError(f"{name} are on {dev} and {d}, expected one GPU")
-        if not contiguous:
-            raise ValueError(f"{name} must be contiguous")
-    if len({k[0] for k in kinds}) == 1:
-        types = array.array("i", [_TYPES[grads[0].dtype]]) * len(grads)
-    else:
-        types = array.array("i", [_TYPES[t.dtype] for t in grads])
-    return dev, [t.numel() for t in grads], types
+    if not all(map(torch.Tensor.is_contiguous, grads)):
+        raise ValueError(f"{name} must be contiguous")
+    types = ([_TYPES[dtypes.pop()]] * len(grads) if len(dtypes) == 1 else
+             [_TYPES[t.dtype] for t in grads])
+    return (dev, array.array("Q", map(torch.Tensor.data_ptr, grads)),
+            array.array("q", map(torch.Tensor.numel, grads)), array.array("i", types))
 
 
 def _ptr_of(a: "array.array") -> int:
@@ -385,46 +409,39 @@ def _ptr_of(a: "array.array") -> int:
 
 def _clip_call(grads, max_norm, out, ws, stream):
     grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
-    for g in grads:
-        if not isinstance(g, torch.Tensor):
-            raise TypeError("gradients must be torch tensors")
-    if max_norm is not None and not float(max_norm) >= 0.0:
+    if max_norm is not None and not max_norm >= 0.0:
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
     if not grads:
         raise ValueError("there are no gradients")
-    dev, sizes, types = _grad_arrays("gradients", grads)
-    ptrs = _addresses([g.data_ptr() for g in grads])
-    outs = None
+    dev, ptrs, sizes, types = _grad_arrays("gradients", grads)
+    n, outs = len(grads), None
     if isinstance(out, torch.Tensor):
-        if out.dtype != grads[0].dtype or any(t != types[0] for t in types):
+        dt = grads[0].dtype
+        if out.dtype != dt or types.count(types[0]) != n:
             raise TypeError("a flat out takes gradients of its own dtype only")
-        _same("out", out, (sum(sizes),), (grads[0].dtype,), dev)
-        at, step, each = out.data_ptr(), out.element_size(), []
-        for n in sizes:
-            each.append(at)
-            at += n * step
-        outs = _addresses(each)
+        _same("out", out, (sum(sizes),), (dt,), dev)
+        step = out.element_size()
+        outs = array.array("Q", itertools.accumulate(map(step.__mul__, sizes),
+                                                     initial=out.data_ptr()))
     elif out is not None:
         out = list(out)
-        if len(out) != len(grads):
-            raise ValueError(f"out has {len(out)} tensors for {len(grads)} gradients")
+        if len(out) != n:
+            raise ValueError(f"out has {len(out)} tensors for {n} gradients")
         for g, o in zip(grads, out):
             _same("out", o, g.shape, (g.dtype,), dev)
-        outs = _addresses([o.data_ptr() for o in out])
-    nbytes = array.array("q", sizes)
-    n = len(grads)
+        outs = array.array("Q", [o.data_ptr() for o in out])
     st, ctx = _on(dev, stream)
     with ctx:
         norm_out = torch.empty(1, dtype=torch.float32, device=dev)
         L = lib()
         ws = _scratch(int(L.qlora_clip_workspace_size(n)), dev, ws)
         if max_norm is None:
-            check(L.qlora_grad_norm(n, _ptr_of(ptrs), _ptr_of(nbytes), _ptr_of(types),
+            check(L.qlora_grad_norm(n, _ptr_of(ptrs), _ptr_of(sizes), _ptr_of(types),
                                     norm_out.data_ptr(), ws.data_ptr(), _bytes(ws), st),
                   "qlora_grad_norm")
         else:
-            check(L.qlora_clip_grad_norm(n, _ptr_of(ptrs), _ptr_of(nbytes), _ptr_of(types),
-                                         float(max_norm), None if outs is None else _ptr_of(outs),
+            check(L.qlora_clip_grad_norm(n, _ptr_of(ptrs), _ptr_of(sizes), _ptr_of(types),
+                                         max_norm, None if outs is None else _ptr_of(outs),
                                          norm_out.data_ptr(), ws.data_ptr(), _bytes(ws), st),
                   "qlora_clip_grad_norm")
     return norm_out
