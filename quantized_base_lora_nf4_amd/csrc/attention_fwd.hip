@@ -34,8 +34,22 @@ struct FwdState {
 template <int DP>
 __device__ __forceinline__ void fwd_tile(FwdState<DP>& st, const uint16_t* kt, const uint16_t* vt,
                                          const FragOff& f, bool mask, int last, int half) {
-  constexpr int T = Geo<DP>::kDT;
-  f32x16 s[2] = {rows_times<DP>(kt, st.q, f, 0), rows_times<DP>(kt, st.q, f, 1)};
+  constexpr int T = Geo<DP>::kDT, S = Geo<DP>::kSteps, kAhead = 2;
+  const int row = opaque(f.row);
+  f32x16 s[2] = {f32x16{}, f32x16{}};
+  float top = -kInf;
+  {
+    bf16x8 x[2 * S];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = read_rows<DP>(kt, row, i, 0);
+    step_fence();
+#pragma unroll
+    for (int i = 0; i < 2 * S; ++i) {
+      if (i + kAhead < 2 * S) x[i + kAhead] = read_rows<DP>(kt, row, (i + kAhead) % S, (i + kAhead) / S);
+      s[i / S] = mfma32(x[i], st.q[i % S], s[i / S]);
+      step_fence();
+    }
+  }
   if (mask) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -43,7 +57,6 @@ __device__ __forceinline__ void fwd_tile(FwdState<DP>& st, const uint16_t* kt, c
       for (int v = 0; v < 16; ++v)
         if (32 * r + elem_row(v, half) > last) s[r][v] = -kInf;
   }
-  float top = -kInf;
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -62,29 +75,37 @@ __device__ __forceinline__ void fwd_tile(FwdState<DP>& st, const uint16_t* kt, c
   }
   const float m = st.m == -kInf ? 0.0f : st.m;
   const int tr = opaque(f.tr);
-  constexpr int N = 4 * T, kAhead = 2;
+  constexpr int N = 4 * T;
   bf16x8 x[N];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) x[j] = read_tr<DP>(vt, tr, j % T, j / T);
   float sum = 0.0f;
   u32x4 pw[4];
+  // word w (elements 2 w, 2 w + 1 of the 32 of this lane) of the probabilities
+  auto prob = [&](int w) {
+    const int r = w / 8, v = 2 * (w % 8);
+    const float a = __builtin_amdgcn_exp2f(fmaf(s[r][v], st.c, -m));
+    const float b = __builtin_amdgcn_exp2f(fmaf(s[r][v + 1], st.c, -m));
+    sum += a;
+    sum += b;
+    pw[w / 4][w % 4] = pack_bf16x2(a, b);
+  };
+  // The first 32 rows' probabilities, then the others' between the products
+  // with the first.
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      s[r][v] = __builtin_amdgcn_exp2f(fmaf(s[r][v], st.c, -m));
-      sum += s[r][v];
-    }
-  st.l += sum;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) pw[b] = __builtin_bit_cast(u32x4, pack8(s[b >> 1], b & 1));
+  for (int w = 0; w < 8; ++w) prob(w);
   step_fence();
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (j + kAhead < N) x[j + kAhead] = read_tr<DP>(vt, tr, (j + kAhead) % T, (j + kAhead) / T);
     st.o[j % T] = mfma32(x[j], as_bf16x8(pw[j / T]), st.o[j % T]);
+    if (j < N / 2) {
+#pragma unroll
+      for (int w = 16 * j / N; w < 16 * (j + 1) / N; ++w) prob(8 + w);
+    }
     step_fence();
   }
+  st.l += sum;
 }
 
 template <int DP>
