@@ -81,12 +81,10 @@ __device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
 
 // Dense: every sequence has the same tiles, ntiles = ceil(cols / kBlock).
 // Packed: `slots` tiles per head, at least as many as all sequences have.
-// Up to 63 sequences, the tiles are taken by the length of their walk, the
-// longest first: with a causal mask a sequence of n tiles has one of each
-// length 1 .. n, so the tiles of one length are found by a ballot over the
-// sequences; without one, all its tiles have length n.  With more sequences
-// the tiles are taken sequence by sequence (64 lengths at a time, by a prefix
-// sum over the wave).
+// They are taken sequence by sequence, so that tiles which share K and V run
+// at the same time; up to 63 sequences, those with the most tiles first (by a
+// ballot for each count), so that no long walk starts last; with more, in
+// their order (64 lengths at a time, by a prefix sum over the wave).
 // After the last sequence, the rows that belong to none form one more, with
 // nothing on the other side, so that outputs are zero there.  Offsets are
 // clamped to the tensors' rows, so that wrong ones give wrong results but no
@@ -135,13 +133,13 @@ __device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned
     }
     int left = slot;
     for (int len = __builtin_amdgcn_readfirstlane(longest); len > 0; --len) {
-      uint64_t has = __ballot(p.causal ? n >= len : n == len);
-      const int each = p.causal ? 1 : len, count = __popcll(has) * each;
+      uint64_t has = __ballot(n == len);
+      const int count = __popcll(has) * len;
       if (left < count) {
-        for (int i = left / each; i > 0; --i) has &= has - 1;
+        for (int i = left / len; i > 0; --i) has &= has - 1;
         found = __ffsll((unsigned long long)has) - 1;
-        w.ntiles = __builtin_amdgcn_readlane(n, found);
-        tile = p.causal ? w.ntiles - len : left % each;
+        w.ntiles = len;
+        tile = left % len;
         break;
       }
       left -= count;
