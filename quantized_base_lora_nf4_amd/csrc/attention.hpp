@@ -193,6 +193,12 @@ __device__ __forceinline__ int opaque(int v) {
   return v;
 }
 
+// The lane, computed anew: two instructions instead of a register that lives
+// through the loop.
+__device__ __forceinline__ int lane_now() {
+  return opaque(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)));
+}
+
 // A wave-uniform float in a scalar register.
 __device__ __forceinline__ float uniform(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));

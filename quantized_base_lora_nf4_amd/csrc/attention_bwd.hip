@@ -177,11 +177,11 @@ __device__ __forceinline__ void each16(F&& f, std::integer_sequence<int, I...>) 
 template <int DP>
 __device__ __forceinline__ void dkv_tile(DkvState<DP>& st, const uint16_t* qt, const uint16_t* gt,
                                          const float* stats, int left, const FragOff& f, bool mask,
-                                         int from, int half, int lane) {
+                                         int from) {
   constexpr int T = Geo<DP>::kDT;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const int tr = opaque(f.tr);
+    const int tr = opaque(f.tr), lane = lane_now(), half = lane >> 5;
     const int i = 32 * r + elem_row(lane & 15, half);
     float lse = stats[i];
     const float delta = stats[kTile + i];
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
     if (first >= w.lk) return;
     if (p.causal && r0 + kTile - 1 + off < first) return;
     const bool mask = p.causal && r0 + off < first + kCols - 1;
-    dkv_tile<DP>(st, qt, gt, stats, w.lq - r0, f, mask, rowc - off - r0, half, lane);
+    dkv_tile<DP>(st, qt, gt, stats, w.lq - r0, f, mask, rowc - off - r0);
   };
   for (int n = n0; n < n1; n += 2) {
     tiles_ready();
