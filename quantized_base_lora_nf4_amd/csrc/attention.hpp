@@ -16,9 +16,9 @@
 // output columns leaves 8 consecutive output elements in a lane, so
 // results are stored 16 bytes at a time.
 //
-// Tiles in LDS are [64][DP] bf16, DP = 64 or 128 (the head dimension rounded
-// up; dimensions past D hold copies of valid ones, meet zeros in the
-// register operand, and are not stored).  The 16-byte chunks of a row are
+// The products take the head dimension rounded up to DP = 64, 96 or 128;
+// tiles in LDS are [64][64 or 128] bf16 (dimensions past D hold copies of
+// valid ones, meet zeros in the register operand, and are not stored).  The 16-byte chunks of a row are
 // stored in the order chunk ^ mask(row), chosen so that both ways of
 // reading are free of bank conflicts: 16 rows of one chunk (ds_read_b128)
 // and 4 + 4 rows of 4 chunks (the transposing ds_read_b64_tr_b16).
@@ -178,6 +178,16 @@ __device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned
   return w;
 }
 
+// Calls f(DP) for a head dimension.
+template <int V>
+struct Dim {
+  static constexpr int value = V;
+};
+template <class F>
+hipError_t with_dim(int D, F&& f) {
+  return D <= 64 ? f(Dim<64>{}) : D <= 96 ? f(Dim<96>{}) : f(Dim<128>{});
+}
+
 // Tiles per head to launch for `cols` columns.
 inline int64_t tile_slots(const AttnArgs& a, int64_t cols) {
   const int64_t n = (cols + kBlock - 1) / kBlock;
@@ -204,10 +214,12 @@ __device__ __forceinline__ float uniform(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 
+// DP = 64, 96 or 128: the head dimension as the products see it.
 template <int DP>
 struct Geo {
-  static constexpr int kChunks = DP / 8;           // 16-byte chunks per row
-  static constexpr int kElems = kTile * DP;        // elements of a tile
+  static constexpr int kPitch = DP <= 64 ? 64 : 128;  // elements of a row in LDS
+  static constexpr int kChunks = kPitch / 8;       // 16-byte chunks per row
+  static constexpr int kElems = kTile * kPitch;    // elements of a tile
   static constexpr int kSteps = DP / 16;           // 16-deep contraction steps over the dimension
   static constexpr int kDT = DP / 32;              // 32-wide tiles of the dimension
   // 16-byte loads per thread that fill a tile
@@ -217,7 +229,7 @@ struct Geo {
 // Chunk mask of a row (see above).
 template <int DP>
 __device__ __forceinline__ int chunk_mask(int row) {
-  if constexpr (DP == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  if constexpr (Geo<DP>::kPitch == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
   else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
 }
 
@@ -305,14 +317,15 @@ struct FragOff {
 // of the dimension that A row 16 (g % 2) + j stands for.
 template <int DP>
 __device__ __forceinline__ FragOff frag_off(int lane) {
+  constexpr int P = Geo<DP>::kPitch;
   FragOff f;
   const int r = swap23(lane & 31);
-  f.row = r * DP * 2 + (((lane >> 5) ^ chunk_mask<DP>(r)) << 4);
+  f.row = r * P * 2 + (((lane >> 5) ^ chunk_mask<DP>(r)) << 4);
   const int g = lane >> 4, j = lane & 15;
   const int x = 4 * (g & 1) + (j & 3);                       // which 4 A rows
   const int x4 = (x & 4) | ((x & 1) << 1) | ((x >> 1) & 1);  // the 4 dimensions they stand for
   const int rt = 8 * (g >> 1) + (j >> 2);
-  f.tr = rt * DP * 2 + (((x4 >> 1) ^ chunk_mask<DP>(rt)) << 4) + 8 * (x4 & 1);
+  f.tr = rt * P * 2 + (((x4 >> 1) ^ chunk_mask<DP>(rt)) << 4) + 8 * (x4 & 1);
   return f;
 }
 
@@ -321,7 +334,7 @@ __device__ __forceinline__ FragOff frag_off(int lane) {
 template <int DP>
 __device__ __forceinline__ bf16x8 read_rows(const uint16_t* tile, int row, int s, int rt) {
   return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(tile) + (row ^ (s << 5)) +
-                                          rt * 64 * DP);
+                                          rt * 64 * Geo<DP>::kPitch);
 }
 
 // Tile rows 16 slab + 8 (lane / 32) + 0..7 of dimension 32 d + swap23(lane % 32),
@@ -331,11 +344,11 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* tile, int tr, int d, i
   typedef short v4i16 __attribute__((ext_vector_type(4)));
   typedef short v8i16 __attribute__((ext_vector_type(8)));
   typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-  const char* t = reinterpret_cast<const char*>(tile) + slab * 32 * DP;
+  const char* t = reinterpret_cast<const char*>(tile) + slab * 32 * Geo<DP>::kPitch;
   const int o = tr ^ (d << 6);
   // the row 4 further on has the lowest bit of its chunk mask flipped
   const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + o));
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + (o ^ 16) + 8 * DP));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + (o ^ 16) + 8 * Geo<DP>::kPitch));
   const v8i16 v = v8i16{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8, v);
 }

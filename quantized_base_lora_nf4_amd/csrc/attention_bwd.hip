@@ -370,7 +370,7 @@ hipError_t launch_attn_bwd(const AttnArgs& args, float* ws, hipStream_t stream) 
   if (!a.cu_q && a.nseq == 0) return hipSuccess;
   a.delta = ws;
   a.part = ws + (a.Sq * a.H * (a.cu_q ? 1 : a.nseq) + 3) / 4 * 4;
-  return a.D <= 64 ? launch_bwd<64>(a, stream) : launch_bwd<128>(a, stream);
+  return with_dim(a.D, [&](auto dim) { return launch_bwd<decltype(dim)::value>(a, stream); });
 }
 
 }  // namespace qn

@@ -165,9 +165,10 @@ hipError_t launch_attn_fwd(const AttnArgs& args, float* ws, hipStream_t stream) 
   a.part = ws;
   a.part_lse = ws + a.splits * heads * a.Sq * a.D;
   const unsigned grid = (unsigned)(slots * heads * a.splits);
-  if (a.D <= 64) k_attn_fwd<64><<<grid, kWaves * 64, 0, stream>>>(a, (int)slots);
-  else k_attn_fwd<128><<<grid, kWaves * 64, 0, stream>>>(a, (int)slots);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = with_dim(a.D, [&](auto dim) {
+    k_attn_fwd<decltype(dim)::value><<<grid, kWaves * 64, 0, stream>>>(a, (int)slots);
+    return hipGetLastError();
+  });
   return e != hipSuccess || a.splits == 1 ? e : launch_attn_join_fwd(a, stream);
 }
 
