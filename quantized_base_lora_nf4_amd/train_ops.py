@@ -15,6 +15,7 @@ import operator
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, check, lib
 from .ops import _stream_obj
@@ -222,7 +223,7 @@ def _takeable(t: torch.Tensor) -> torch.Tensor:
     """t, or a copy if its strides are not ones the kernels take."""
     st = t.stride()
     ok = st[-1] == 1 and all(s % 8 == 0 for s in st[:-1]) and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 class _AttentionFunction(torch.autograd.Function):
@@ -234,6 +235,7 @@ class _AttentionFunction(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_seqlens, cu_seqlens_k = ctx.saved_tensors
         grads = attention_bwd(q, k, v, o, lse, _takeable(do), *ctx.how, cu_seqlens, cu_seqlens_k)
@@ -332,6 +334,7 @@ class _NormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -459,7 +462,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, ws: Optional[torch.Tensor] 
     """Scale the gradients by min(1, max_norm / (norm + 1e-6)) and return
     their norm before that (a one-element float32 device tensor).
 
-    out: None scales in place; a list of tensors (one per gradient that is
+    Each gradient is given once.  out: None scales in place; a list of tensors (one per gradient that is
     not None, same shape and dtype) takes the scaled gradients instead, and
     so does one flat tensor of their dtype, one gradient after the other."""
     return _clip_call(grads, float(max_norm), out, ws, stream)
