@@ -68,7 +68,7 @@ def train(block, x, target, cu_seqlens, steps, lr=2e-3, max_norm=0.3, report=pri
         norms.append(qn.clip_grad_norm([p.grad for p in params], max_norm))
         opt.step()
         losses.append(loss.detach())
-        report(f"step {step}: loss {float(loss):.5f}, gradient norm {float(norms[-1]):.4f}")
+        report(f"step {step}: loss {float(losses[-1]):.5f}, gradient norm {float(norms[-1]):.4f}")
     return [float(v) for v in losses], [float(v) for v in norms]
 
 

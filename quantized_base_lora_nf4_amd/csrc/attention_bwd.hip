@@ -16,6 +16,21 @@
 //
 // P and dS are rounded to bf16 as operands of the products that follow
 // (fp32 sums), everything else is fp32.
+//
+// Both kernels run two workgroups of four waves per CU, within 256 registers
+// per lane.  In the dK/dV kernel 192 of them hold K, V, dK and dV; the rest is
+// enough because scores and dO V^T are computed 32 x 32 at a time, one after
+// the other, the row statistics come by lane broadcast from two registers,
+// and addresses are made anew in every step.  (With all reads moved ahead by
+// the compiler the same kernel needed 512 registers, one wave per SIMD, or
+// reloads that wait for the next tile: 1446 to 2100 us instead of 1000.)
+//
+// Measured (one sequence of 8192 tokens, 32 heads over 8 key/value heads of
+// 128, causal): dQ 687 us, dK/dV 998 us and 25 us to join its two shares;
+// 1716 us in all, 1120 TFLOP/s over the seven products against 1280 to 1390 of
+// large library products; MFMA pipes busy 59 to 63 % of the cycles at the 1.8 GHz
+// that the chip holds, so the clock (power) bounds them.  8 x 512 tokens,
+// 32 heads: 54 and 66 us; their loads and stores alone take 43 and 41 us.
 #include <utility>
 
 #include "attention.hpp"

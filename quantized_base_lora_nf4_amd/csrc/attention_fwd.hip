@@ -11,6 +11,19 @@
 //
 // P is rounded to bf16 for the product with V (the MFMA's input type; fp32
 // sums); the row sum l adds the fp32 values.
+//
+// Four waves of 32 queries share a workgroup's K and V tiles; two workgroups
+// fit on a CU (64 KB of LDS and 211 registers each at 128 dimensions), so that
+// one's exponentials run beside the other's products.  The waits and fences
+// in the tile keep operand reads two steps ahead of the products and no
+// further: the registers that reads further ahead would take are the second
+// wave's.
+//
+// Measured (one sequence of 8192 tokens, 32 heads over 8 key/value heads of
+// 128, causal): 513 us, 1070 TFLOP/s against 1280 to 1390 of large bf16
+// library products on the same card; the MFMA pipes are busy 52 % of the
+// cycles at the 1.84 GHz that the chip holds.  8 x 512 tokens, 32 heads: 40 us;
+// the tile loads alone, without the arithmetic, take 30 us (135 MB).
 #include "attention.hpp"
 
 namespace qn {

