@@ -125,15 +125,24 @@ __device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned
   };
   if (p.nseq < 64) {
     n = tiles_of(lane);
-    int longest = n;
+    // the largest count below `than` (0: none)
+    auto largest = [&](int than) {
+      int v = n < than ? n : 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const int other = __shfl_xor(longest, o, 64);
-      longest = longest > other ? longest : other;
-    }
+      for (int o = 32; o > 0; o >>= 1) {
+        const int other = __shfl_xor(v, o, 64);
+        v = v > other ? v : other;
+      }
+      return __builtin_amdgcn_readfirstlane(v);
+    };
     int left = slot;
-    for (int len = __builtin_amdgcn_readfirstlane(longest); len > 0; --len) {
+    for (int len = largest(0x7fffffff); len > 0; --len) {
       uint64_t has = __ballot(n == len);
+      if (!has) {  // a gap: on to the next count that there is
+        len = largest(len);
+        if (len == 0) break;
+        has = __ballot(n == len);
+      }
       const int count = __popcll(has) * len;
       if (left < count) {
         for (int i = left / len; i > 0; --i) has &= has - 1;
