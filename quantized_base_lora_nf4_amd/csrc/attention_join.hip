@@ -10,6 +10,8 @@
 // and a second kernel adds them in a fixed order (8192 tokens, 8 key/value
 // heads, causal: dK/dV 1318 us unshared, 998 + 25 us shared by two; the join
 // moves 134 MB at 5.4 TB/s).
+#include <math.h>
+
 #include "attention.hpp"
 
 namespace qn {
@@ -91,11 +93,13 @@ __global__ __launch_bounds__(256) void k_attn_join_sum(const float* part, int sp
 }  // namespace
 
 // The split that the following estimate finds fastest.  Times in us, from
-// measurements at D = 128 (D <= 64: half): a step (64 rows of the walk) takes
-// a workgroup 4.0 while two share a CU (all three passes within 20 %), 2.6 alone;
-// starting and storing a tile about 4; a join about 6 and its partial results'
-// bytes, written and read, at 4 TB/s.  Packed lengths are known to the
-// device only: they are taken to be equal.
+// measurements at D = 128 (in proportion for 64 and 96): a step (64 rows of the
+// walk) takes a workgroup 2.1 in the forward, 2.8 in dQ and 4.0 in dK/dV while
+// two share a CU, and about 0.65 of that alone; starting and storing a tile
+// about 4; a join about 6 and its partial results' bytes, written and read, at
+// 4 TB/s.  Packed lengths are known to the device only: for n sequences cut at
+// random the longest is taken to be 1 + log2(n) / 2 times the mean, and a
+// tile's mean walk up to 1.8 times.
 int attn_splits(const AttnArgs& a, AttnPass pass) {
   const bool keys = pass == kAttnDkv;
   const int64_t cols = keys ? a.Sk : a.Sq, walk = keys ? a.Sq : a.Sk;
@@ -106,15 +110,18 @@ int attn_splits(const AttnArgs& a, AttnPass pass) {
   const int64_t len = a.cu_q ? (walk + n - 1) / n : walk;
   const int64_t steps = (len + kTile - 1) / kTile * (keys ? a.H / a.Hkv : 1);
   if (tiles < 1 || tiles > 65536 || steps < 2) return 1;
-  const double unit = a.D <= 64 ? 0.5 : 1.0;
-  const double total = (double)tiles * steps * (a.causal ? 0.55 : 1.0);
+  const double unit = (pass == kAttnFwd ? 2.1 : pass == kAttnDq ? 2.8 : 4.0) *
+                      (a.D <= 64 ? 0.5 : a.D <= 96 ? 0.75 : 1.0);
+  const double uneven = a.cu_q ? 1.0 + 0.5 * log2((double)n) : 1.0;
+  const double total =
+      (double)tiles * steps * (uneven < 1.8 ? uneven : 1.8) * (a.causal ? 0.55 : 1.0);
   const double bytes = (double)all_rows(a, pass) * a.D * 8.0 * (keys ? 2 : 1);
   int best = 1;
   double best_t = 0.0;
   for (int s = 1; s <= 32 && s <= steps; s = s < 4 ? s + 1 : s + s / 2) {
-    const double longest = (double)((steps + s - 1) / s);
+    const double longest = (double)((steps + s - 1) / s) * uneven;
     const double slots = tiles * s < kResident ? (double)(tiles * s) : (double)kResident;
-    const double step = unit * (tiles * s > kResident / 2 ? 4.0 : 2.6);
+    const double step = unit * (tiles * s > kResident / 2 ? 1.0 : 0.65);
     const double rounds = total / s > 0 ? total / slots : 0.0;
     double t = (rounds > longest ? rounds : longest) * step +
                4.0 * (double)(tiles * s) / slots;
