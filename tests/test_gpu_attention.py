@@ -284,8 +284,8 @@ def test_scale_and_another_stream():
 
 def test_shared_walks_are_the_same_on_every_run():
     say("[attention] shared walks, determinism")
-    q, do = draw(1, 1, 1000, 4, 64), draw(2, 1, 1000, 4, 64)
-    k, v = draw(3, 1, 1000, 1, 64), draw(4, 1, 1000, 1, 64)
+    q, do = draw(1, 1, 1000, 4, 128), draw(2, 1, 1000, 4, 128)
+    k, v = draw(3, 1, 1000, 1, 128), draw(4, 1, 1000, 1, 128)
     c = qn.train_ops._AttnCall(q, k, v, True, None, None, None).c
     assert qn.lib().qlora_attention_fwd_workspace_size(c) > 0
     assert qn.lib().qlora_attention_bwd_workspace_size(c) > 4000 * 4
