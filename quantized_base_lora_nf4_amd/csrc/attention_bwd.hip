@@ -248,7 +248,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
   __shared__ __attribute__((aligned(16))) uint16_t q0[Geo<DP>::kElems], g0[Geo<DP>::kElems];
   __shared__ __attribute__((aligned(16))) uint16_t q1[Geo<DP>::kElems], g1[Geo<DP>::kElems];
   __shared__ float s0[2 * kTile], s1[2 * kTile];  // lse, then D, of the tile's rows
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Work w = find_work<true>(p, slots, p.Hkv);
   if (!w.valid) return;
