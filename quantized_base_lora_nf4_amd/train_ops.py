@@ -65,11 +65,6 @@ def _bytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _new_like(t: torch.Tensor) -> torch.Tensor:
-    """An uninitialized contiguous bf16 tensor of t's shape."""
-    return torch.empty_like(t, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
-
-
 def _scratch(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
     if ws is not None:
         if ws.device != device or not ws.is_contiguous():
@@ -83,21 +78,45 @@ def _scratch(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
 # Attention
 # ---------------------------------------------------------------------------
 
+def _heads(name, t, shape, device, packed) -> tuple:
+    """(address, batch, row and head stride), as qlora_heads_t, of one
+    [batch, row, head, dim] (packed: [row, head, dim]) tensor of any strides
+    that the kernels take."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.device == device:
+        st = t.stride()
+        if t.dtype in _SIXTEEN and st[-1] == 1 and not (st[-2] | st[-3] | st[0]) & 7:
+            return (t.data_ptr(), 0 if packed else st[0], st[-3], st[-2])
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in _SIXTEEN:
+        raise TypeError(f"{name} must be bf16 (or its 16-bit view), got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.numel() == 0:
+        return (0, 0, 0, 0)
+    # the stride of a dimension of size 1 says nothing
+    st = [0 if n == 1 else s for n, s in zip(shape, t.stride()[:-1])]
+    if (t.stride()[-1] != 1 and shape[-1] != 1) or any(s % 8 for s in st):
+        raise ValueError(f"{name} needs contiguous head vectors and strides of a multiple of 8, "
+                         f"has {t.stride()}")
+    return (t.data_ptr(), 0 if packed else st[0], st[-2], st[-1])
+
+
 class _AttnCall:
-    """Checked arguments of an attention call.  Its tensors' (address, batch,
-    row and head stride) lie one after the other in `words`, as qlora_heads_t."""
+    """Checked arguments of an attention call."""
 
     def __init__(self, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
-        dev = _device_of("q", q)
-        self.packed = cu_seqlens is not None
-        if not self.packed and cu_seqlens_k is not None:
+        self.dev = dev = _device_of("q", q)
+        self.packed = packed = cu_seqlens is not None
+        if not packed and cu_seqlens_k is not None:
             raise ValueError("cu_seqlens_k needs cu_seqlens")
-        nd = 3 if self.packed else 4
+        nd = 3 if packed else 4
         for name, t in (("q", q), ("k", k)):
             if not isinstance(t, torch.Tensor) or t.dim() != nd:
                 raise ValueError(f"{name} must have {nd} dimensions "
-                                 f"({'[row, head, dim]' if self.packed else '[batch, row, head, dim]'})")
-        self.dev = dev
+                                 f"({'[row, head, dim]' if packed else '[batch, row, head, dim]'})")
         self.q_shape = qs = q.shape
         ks = k.shape
         h, d = qs[-2], qs[-1]
@@ -105,7 +124,7 @@ class _AttnCall:
         if h < 1 or hk < 1 or h % hk:
             raise ValueError(f"{h} query heads cannot share {hk} key/value heads")
         cq = ck = None
-        if self.packed:
+        if packed:
             self.k_shape = (ks[0], hk, d)
             if cu_seqlens_k is None:
                 cu_seqlens_k = cu_seqlens
@@ -125,33 +144,20 @@ class _AttnCall:
         if scale is None:
             scale = 1.0 / math.sqrt(d) if d else 1.0
         self.c = Attention(n, qs[-3], ks[-3], cq, ck, h, hk, d, int(causal), float(scale))
-        self.words = []
-        self.add("q", q, self.q_shape)
-        self.add("k", k, self.k_shape)
-        self.add("v", v, self.k_shape)
+        # the tensors' descriptions, one after the other
+        self.words = [*_heads("q", q, qs, dev, packed), *_heads("k", k, self.k_shape, dev, packed),
+                      *_heads("v", v, self.k_shape, dev, packed)]
 
-    def add(self, name, t, shape) -> None:
-        """One more [batch, row, head, dim] (packed: [row, head, dim]) tensor,
-        of any strides that the kernels take."""
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch tensor")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype not in _SIXTEEN:
-            raise TypeError(f"{name} must be bf16 (or its 16-bit view), got {t.dtype}")
-        if t.device != self.dev:
-            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
-        if t.numel() == 0:
-            self.words += (0, 0, 0, 0)
-            return
-        st = t.stride()
-        if st[-1] != 1 or (st[-2] | st[-3] | st[0]) & 7:
-            # the stride of a dimension of size 1 says nothing
-            st = [0 if n == 1 else s for n, s in zip(shape, st[:-1])] + [st[-1]]
-            if (st[-1] != 1 and shape[-1] != 1) or any(s % 8 for s in st[:-1]):
-                raise ValueError(f"{name} needs contiguous head vectors and strides of a multiple "
-                                 f"of 8, has {t.stride()}")
-        self.words += (t.data_ptr(), 0 if self.packed else st[0], st[-3], st[-2])
+    def add(self, name, t, keys: bool) -> None:
+        """One more tensor of the queries' or keys' shape."""
+        self.words += _heads(name, t, self.k_shape if keys else self.q_shape, self.dev, self.packed)
+
+    def new(self, like, keys: bool) -> torch.Tensor:
+        """A new tensor of the queries' or keys' shape, added."""
+        t = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+        _, rows, h, d = (0, *t.shape) if self.packed else t.shape
+        self.words += (t.data_ptr(), 0 if self.packed else rows * h * d, h * d, d)
+        return t
 
     def views(self):
         """The addresses of the tensors' descriptions, in the order added."""
@@ -179,12 +185,13 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
     st, ctx = _on(c.dev, stream)
     with ctx:
         if out is None:
-            out = _new_like(q)
+            out = c.new(q, False)
+        else:
+            c.add("out", out, False)
         lse = torch.empty(c.lse_shape, dtype=torch.float32, device=c.dev)
         L = lib()
-        need = int(L.qlora_attention_fwd_workspace_size(c.c))
+        need = L.qlora_attention_fwd_workspace_size(c.c)
         ws = _scratch(need, c.dev, ws) if need else None
-        c.add("out", out, c.q_shape)
         check(L.qlora_attention_fwd(c.c, *c.views(), lse.data_ptr(),
                                     None if ws is None else ws.data_ptr(), _bytes(ws), st),
               "qlora_attention_fwd")
@@ -201,20 +208,21 @@ def attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Te
     three tensors to write."""
     c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     _same("lse", lse, c.lse_shape, (torch.float32,), c.dev)
-    c.add("o", o, c.q_shape)
-    c.add("do", do, c.q_shape)
+    c.add("o", o, False)
+    c.add("do", do, False)
     st, ctx = _on(c.dev, stream)
     with ctx:
         if out is None:
-            out = _new_like(q), _new_like(k), _new_like(k)
-        dq, dk, dv = out
+            dq, dk, dv = c.new(q, False), c.new(k, True), c.new(k, True)
+        else:
+            dq, dk, dv = out
+            c.add("dq", dq, False)
+            c.add("dk", dk, True)
+            c.add("dv", dv, True)
         L = lib()
-        ws = _scratch(int(L.qlora_attention_bwd_workspace_size(c.c)), c.dev, ws)
-        c.add("dq", dq, c.q_shape)
-        c.add("dk", dk, c.k_shape)
-        c.add("dv", dv, c.k_shape)
-        v = c.views()
-        check(L.qlora_attention_bwd(c.c, *v[:4], lse.data_ptr(), *v[4:], ws.data_ptr(),
+        ws = _scratch(L.qlora_attention_bwd_workspace_size(c.c), c.dev, ws)
+        w = c.views()
+        check(L.qlora_attention_bwd(c.c, *w[:4], lse.data_ptr(), *w[4:], ws.data_ptr(),
                                     _bytes(ws), st), "qlora_attention_bwd")
     return dq, dk, dv
 
