@@ -18,10 +18,11 @@
 //
 // The products take the head dimension rounded up to DP = 64, 96 or 128;
 // tiles in LDS are [64][64 or 128] bf16 (dimensions past D hold copies of
-// valid ones, meet zeros in the register operand, and are not stored).  The 16-byte chunks of a row are
-// stored in the order chunk ^ mask(row), chosen so that both ways of
-// reading are free of bank conflicts: 16 rows of one chunk (ds_read_b128)
-// and 4 + 4 rows of 4 chunks (the transposing ds_read_b64_tr_b16).
+// valid ones, meet zeros in the register operand, and are not stored).  The
+// 16-byte chunks of a row are stored in the order chunk ^ mask(row), chosen
+// so that both ways of reading are free of bank conflicts: 16 rows of one
+// chunk (ds_read_b128, measured 208 bytes per clock and CU) and 4 + 4 rows of
+// 4 chunks (the transposing ds_read_b64_tr_b16: 188; 62 in plain order).
 #pragma once
 
 #include "kernels.hpp"
@@ -241,8 +242,6 @@ __device__ __forceinline__ int chunk_mask(int row) {
   if constexpr (Geo<DP>::kPitch == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
   else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
 }
-
-typedef __attribute__((address_space(3))) uint16_t lds_u16;
 
 // This wave's loads of a tile: load i fills 1024 consecutive bytes of LDS
 // (kRows rows) at row (i kWaves + wave) kRows, lane l's 16 bytes at 16 l, so the

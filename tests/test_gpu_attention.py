@@ -193,6 +193,7 @@ PACKED = [
     ([3] * 150, 1, 1, 64, True, 5),             # more sequences than lanes
     ([129, 257, 511], 5, 5, 80, True, 1),
     ([900, 3, 1100], 4, 1, 128, True, 150),     # shared walks
+    ([2, 1700, 1, 140, 1, 300], 2, 2, 64, True, 0),  # tile counts far apart
 ]
 
 
@@ -220,6 +221,29 @@ def test_packed_with_other_keys():
     k, v = draw(3, sum(lk), 2, 64), draw(4, sum(lk), 2, 64)
     for causal in (True, False):
         check_all(q, k, v, do, causal, cu=cq, cu_k=ck)
+
+
+def test_packed_without_sequences():
+    say("[attention] packed, no sequences")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k = draw(1, 200, 2, 64), draw(2, 200, 1, 64)
+    o, lse = qn.attention_fwd(q, k, k, cu_seqlens=cu)
+    dq, dk, dv = qn.attention_bwd(q, k, k, o, lse, q, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert not o.any() and torch.isneginf(lse).all()
+    assert not dq.any() and not dk.any() and not dv.any()
+
+
+def test_offsets_that_are_wrong_stay_inside_the_tensors():
+    """Negative, descending and too large offsets: outputs are undefined, but
+    every access stays within the rows (the kernels clamp)."""
+    say("[attention] wrong offsets")
+    q, k = draw(1, 300, 2, 64), draw(2, 300, 1, 64)
+    for bad in ([0, 400, 300], [-5, 100, 300], [0, 200, 100], [250, 20, 299], [0, 1 << 30, -(1 << 30)]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        o, lse = qn.attention_fwd(q, k, k, cu_seqlens=cu)
+        qn.attention_bwd(q, k, k, o, lse, q, cu_seqlens=cu)
+    torch.cuda.synchronize()
 
 
 def test_neighbours_of_a_sequence_never_reach_it():

@@ -87,6 +87,21 @@ def test_gradients_at_odd_addresses():
         check([flat[a:b] for a, b in zip(cuts, cuts[1:])], 1.0)
 
 
+def test_more_than_2_to_31_elements():
+    say("[clip] 64-bit offsets")
+    n = (1 << 31) + 20001
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    tail = draw(1, 30000, dtype=torch.bfloat16)
+    g[-30000:] = tail
+    small = draw(2, 5)
+    ref_norm, ref = norms.clip([host(tail), host(small)], 1.0)
+    norm = qn.clip_grad_norm([g, small], 1.0)
+    assert abs(float(norm) - ref_norm) <= 2.0 ** -23 * ref_norm
+    check_scaled(g[-30000:], ref[0], g.dtype)
+    check_scaled(small, ref[1], small.dtype)
+    assert not g[:100000].any() and not g[-40000:-30000].any()
+
+
 @pytest.mark.parametrize("std", [1e30, 1e18, 1e-25, 1e-38])
 def test_sizes_whose_squares_leave_fp32(std):
     say(f"[clip] std {std}")

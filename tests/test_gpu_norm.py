@@ -124,6 +124,31 @@ def test_views_at_odd_addresses():
         check(x, w, b, dy, 1e-5, False)
 
 
+def test_more_than_2_to_31_elements():
+    """The last rows of a matrix of 2.3e9 elements, with the first ones' stale
+    neighbours far away, are those of the same rows alone."""
+    say("[norm] 64-bit offsets")
+    rows, width = 70000, 32768
+    x = torch.zeros(rows, width, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[-3:], dy[-3:] = draw(1, 3, width, dtype=x.dtype), draw(2, 3, width, dtype=x.dtype)
+    w = draw(3, width)
+    y, mean, rstd = qn.norm_fwd(x, w)
+    dx, dw, db = qn.norm_bwd(dy, x, w, mean, rstd)
+    y3, mean3, rstd3 = qn.norm_fwd(x[-3:], w)
+    dx3, dw3, db3 = qn.norm_bwd(dy[-3:], x[-3:], w, mean3, rstd3)
+    torch.cuda.synchronize()
+    # other launch shapes for few and many rows: the sums' order differs, so
+    # fp32 statistics agree to 80 * 2^-24 and bf16 results to one rounding
+    assert torch.allclose(rstd[-3:], rstd3, rtol=1e-5) and torch.allclose(mean[-3:], mean3, atol=1e-5)
+    assert not y[:100].any() and not dx[:100].any()
+    for a, b in ((y[-3:], y3), (dx[-3:], dx3)):
+        assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -7, atol=1e-5)
+    # rows of zeros add nothing to the parameters' gradients
+    for a, b in ((dw, dw3), (db, db3)):
+        assert torch.allclose(a, b, rtol=1e-4, atol=1e-4)
+
+
 def test_no_rows():
     say("[norm] no rows")
     x = torch.zeros(0, 40, device="cuda")
