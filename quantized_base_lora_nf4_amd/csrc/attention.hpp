@@ -244,8 +244,8 @@ __device__ __forceinline__ int chunk_mask(int row) {
 }
 
 // This wave's loads of a tile: load i fills 1024 consecutive bytes of LDS
-// (kRows rows) at row (i kWaves + wave) kRows, lane l's 16 bytes at 16 l, so the
-// lane fetches the chunk that the mask puts there: the same one in every load,
+// (R = 64 / kChunks rows) at row (i kWaves + wave) R, lane l's 16 bytes at 16 l,
+// so the lane fetches the chunk that the mask puts there: the same one in every load,
 // since the loads' rows agree in the bits that the mask looks at.  Rows past
 // the last one read the last row again, chunks past D the row's first.
 struct TileLoader {
@@ -356,7 +356,8 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* tile, int tr, int d, i
   const int o = tr ^ (d << 6);
   // the row 4 further on has the lowest bit of its chunk mask flipped
   const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + o));
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + (o ^ 16) + 8 * Geo<DP>::kPitch));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds_v4i16*)(t + (o ^ 16) + 8 * Geo<DP>::kPitch));
   const v8i16 v = v8i16{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8, v);
 }

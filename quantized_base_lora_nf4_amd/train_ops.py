@@ -261,19 +261,18 @@ def attention(q, k, v, causal: bool = True, scale: Optional[float] = None, cu_se
 # Norms
 # ---------------------------------------------------------------------------
 
-def _check_norm(x, weight, others):
+def _check_norm(x, weight):
+    """(device, rows, width) of the rows of x, with the weight checked."""
     dev = _device_of("x", x)
-    if x.dim() < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must have at least 1 dimension")
     if x.dtype not in _TYPES:
         raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    width = x.shape[-1]
-    _same("weight", weight, (width,), tuple(_TYPES), dev)
-    for name, t, shape, dtype in others:
-        if t is not None:
-            _same(name, t, shape, (dtype,), dev)
+    width = shape[-1]
+    _same("weight", weight, (width,), _TYPES, dev)
     return dev, x.numel() // width if width else 0, width
 
 
@@ -286,8 +285,11 @@ def norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     x and y are bfloat16 or float32, weight and bias either (of one type);
     mean and rstd are float32, one per row, and mean is None with `rms`.
     Returns (y, mean, rstd)."""
-    dev, rows, width = _check_norm(x, weight, (
-        ("bias", bias, weight.shape, weight.dtype), ("out", out, x.shape, x.dtype)))
+    dev, rows, width = _check_norm(x, weight)
+    if bias is not None:
+        _same("bias", bias, weight.shape, (weight.dtype,), dev)
+    if out is not None:
+        _same("out", out, x.shape, (x.dtype,), dev)
     st, ctx = _on(dev, stream)
     with ctx:
         if out is None:
@@ -309,11 +311,14 @@ def norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     """(dx, dweight, dbias) of norm_fwd for the output gradient dy, from its
     mean and rstd.  dbias is computed without `rms` unless need_db says
     otherwise; what is not computed is None."""
-    dev, rows, width = _check_norm(x, weight, (
-        ("dy", dy, x.shape, x.dtype), ("rstd", rstd, x.shape[:-1], torch.float32),
-        ("mean", None if rms else mean, x.shape[:-1], torch.float32)))
-    if dy is None or rstd is None or (mean is None and not rms):
-        raise ValueError("dy, rstd and (without rms) mean are needed")
+    dev, rows, width = _check_norm(x, weight)
+    lead = x.shape[:-1]
+    _same("dy", dy, x.shape, (x.dtype,), dev)
+    _same("rstd", rstd, lead, (torch.float32,), dev)
+    if not rms:
+        if mean is None:
+            raise ValueError("mean is needed without rms")
+        _same("mean", mean, lead, (torch.float32,), dev)
     if need_db is None:
         need_db = not rms
     st, ctx = _on(dev, stream)
