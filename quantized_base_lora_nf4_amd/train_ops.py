@@ -65,6 +65,14 @@ def _bytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _floats(shape, device) -> torch.Tensor:
+    """An uninitialized float32 tensor (sizes given one by one: torch takes
+    twice as long over a tuple)."""
+    if shape:
+        return torch.empty(*shape, dtype=torch.float32, device=device)
+    return torch.empty((), dtype=torch.float32, device=device)
+
+
 def _scratch(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
     if ws is not None:
         if ws.device != device or not ws.is_contiguous():
@@ -144,6 +152,7 @@ class _AttnCall:
         if scale is None:
             scale = 1.0 / math.sqrt(d) if d else 1.0
         self.c = Attention(n, qs[-3], ks[-3], cq, ck, h, hk, d, int(causal), float(scale))
+        self.q_rhd = (qs[-3], h, d)
         # the tensors' descriptions, one after the other
         self.words = [*_heads("q", q, qs, dev, packed), *_heads("k", k, self.k_shape, dev, packed),
                       *_heads("v", v, self.k_shape, dev, packed)]
@@ -155,7 +164,7 @@ class _AttnCall:
     def new(self, like, keys: bool) -> torch.Tensor:
         """A new tensor of the queries' or keys' shape, added."""
         t = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
-        _, rows, h, d = (0, *t.shape) if self.packed else t.shape
+        rows, h, d = self.k_shape[-3:] if keys else self.q_rhd
         self.words += (t.data_ptr(), 0 if self.packed else rows * h * d, h * d, d)
         return t
 
@@ -188,7 +197,7 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
             out = c.new(q, False)
         else:
             c.add("out", out, False)
-        lse = torch.empty(c.lse_shape, dtype=torch.float32, device=c.dev)
+        lse = _floats(c.lse_shape, c.dev)
         L = lib()
         need = L.qlora_attention_fwd_workspace_size(c.c)
         ws = _scratch(need, c.dev, ws) if need else None
@@ -294,8 +303,9 @@ def norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     with ctx:
         if out is None:
             out = torch.empty_like(x)
-        mean = None if rms else torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        lead = x.shape[:-1]
+        mean = None if rms else _floats(lead, dev)
+        rstd = _floats(lead, dev)
         check(lib().qlora_norm_fwd(x.data_ptr(), rows, width, _TYPES[x.dtype], weight.data_ptr(),
                                    None if bias is None else bias.data_ptr(),
                                    _TYPES[weight.dtype], float(eps), int(rms), out.data_ptr(),
