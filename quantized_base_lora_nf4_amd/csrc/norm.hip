@@ -226,8 +226,9 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm_fwd(
 // same columns of every row, so its share of dw and db adds up in registers.
 // At the end the groups' shares are added pairwise through LDS, and the
 // workgroup writes one row of partial sums part[2][G][width] (dw, then db if
-// kBias), which k_norm_bwd_params adds in a fixed order.  The next row's loads
-// run during the current one.
+// kBias), which k_norm_bwd_params adds in a fixed order; a single workgroup
+// (few rows) writes dw and db itself.  The next row's loads run during the
+// current one.
 //
 // Few, large workgroups keep the partial rows few: at 256 of them their
 // traffic is 2 % of the pass at 8192 x 8192 and 12 % at 4096 x 1024 (bf16).
@@ -235,7 +236,8 @@ template <class T, class PT, int NT, int TPR, int NV, bool kRms, bool kBias>
 __global__ __launch_bounds__(NT) void k_norm_bwd(
     const typename T::elem* __restrict__ dy, const typename T::elem* __restrict__ x, int64_t rows,
     int width, const typename PT::elem* __restrict__ w, const float* __restrict__ mean,
-    const float* __restrict__ rstd, typename T::elem* __restrict__ dx, float* __restrict__ part) {
+    const float* __restrict__ rstd, typename T::elem* __restrict__ dx, float* __restrict__ part,
+    typename PT::elem* __restrict__ dw, typename PT::elem* __restrict__ db) {
   constexpr int VEC = T::VEC, RG = NT / TPR, W = TPR / 64;
   constexpr int kSums = W > 1 ? 4 * (NT / 64) : 1;            // floats for the row sums
   constexpr int kShare = RG > 1 ? RG / 2 * TPR * NV * VEC : 1;  // and for half of the groups' shares
@@ -374,6 +376,20 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(
     gather(aw);
     if constexpr (kBias) gather(ab);
     if (group > 0) return;
+  }
+  if (gridDim.x == 1) {  // the only partial sums are the sums
+    auto store = [&](typename PT::elem* out, const float (&a)[NV][VEC]) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int col = (i * TPR + t) * VEC + e;
+          if (out && col < width) out[col] = f32_elem<PT>(a[i][e]);
+        }
+    };
+    store(dw, aw);
+    if constexpr (kBias) store(db, ab);
+    return;
   }
   float* pw = part + (int64_t)blockIdx.x * width;
   float* pb = pw + (int64_t)gridDim.x * width;
@@ -536,7 +552,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
             kern<<<G, NT, 0, stream>>>((const typename T::elem*)a.dy,
                                         (const typename T::elem*)a.x, a.rows, (int)a.width,
                                         (const typename PT::elem*)a.w, a.mean, a.rstd,
-                                        (typename T::elem*)a.dx, a.dw || a.db ? a.part : nullptr);
+                                        (typename T::elem*)a.dx, a.dw || a.db ? a.part : nullptr,
+                                        (typename PT::elem*)a.dw, (typename PT::elem*)a.db);
             return hipGetLastError();
           };
           if (a.rms)
@@ -549,7 +566,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     });
     if (e != hipSuccess) return e;
   }
-  if (!a.dw && !a.db) return hipSuccess;
+  if ((!a.dw && !a.db) || G == 1) return hipSuccess;
   return with_norm_type(a.w_type, [&](auto pt) {
     using PT = decltype(pt);
     const dim3 grid((unsigned)((a.width + 63) / 64), a.db ? 2 : 1);
