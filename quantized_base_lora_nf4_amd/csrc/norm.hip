@@ -458,6 +458,13 @@ inline int64_t row_vecs(int64_t width, int type) {
 template <int V>
 using IntC = std::integral_constant<int, V>;
 
+// Workgroups of a forward launch; more rows take further launches.  HIP takes
+// fewer than 2^32 threads along a dimension of the grid (2^26 + 5 rows in one
+// launch of four rows per 256 threads: most rows were never written, and no
+// error came back), which is 2^22 workgroups of 1024.  At a quarter of that a
+// launch lasts far longer than the next one's start takes.
+constexpr int64_t kMaxGrid = 1 << 20;
+
 // Forward: threads per row and vectors per thread.  A wave per row has no
 // barriers and is taken for up to 256 vectors while there are rows enough to
 // fill the chip (16384 x 1024 bf16: 14.1 us against 21.9 with 256 threads);
@@ -521,14 +528,18 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
         using T = decltype(t);
         using PT = decltype(pt);
         constexpr int TPR = decltype(tp)::value, NV = decltype(nv)::value;
-        constexpr int NT = block_threads<TPR>();
-        const unsigned grid = (unsigned)((a.rows + NT / TPR - 1) / (NT / TPR));
+        constexpr int NT = block_threads<TPR>(), RPB = NT / TPR;
         auto go = [&](auto kern) {
-          kern<<<grid, NT, 0, stream>>>((const typename T::elem*)a.x, a.rows, (int)a.width,
-                                        (const typename PT::elem*)a.w,
-                                        (const typename PT::elem*)a.b, a.eps,
-                                        (typename T::elem*)a.y, a.mean, a.rstd);
-          return hipGetLastError();
+          for (int64_t r = 0; r < a.rows; r += kMaxGrid * RPB) {
+            const int64_t n = a.rows - r < kMaxGrid * RPB ? a.rows - r : kMaxGrid * RPB;
+            kern<<<(unsigned)((n + RPB - 1) / RPB), NT, 0, stream>>>(
+                (const typename T::elem*)a.x + r * a.width, n, (int)a.width,
+                (const typename PT::elem*)a.w, (const typename PT::elem*)a.b, a.eps,
+                (typename T::elem*)a.y + r * a.width, a.mean ? a.mean + r : nullptr, a.rstd + r);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+          }
+          return hipSuccess;
         };
         return a.rms ? go(k_norm_fwd<T, PT, TPR, NV, true>)
                      : go(k_norm_fwd<T, PT, TPR, NV, false>);

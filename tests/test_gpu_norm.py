@@ -225,3 +225,30 @@ def test_gradients_against_differences_of_the_forward(rms):
         d = rng.standard_normal(at.shape)
         diff = (f(at + 1e-4 * d) - f(at - 1e-4 * d)) / 2e-4
         assert abs((host(got) * d).sum() - diff) <= 1e-5 * (1 + (np.abs(host(got) * d)).sum())
+
+
+# Rows whose forward launch would have more threads than one grid dimension takes (2^32: four rows
+# per 256 threads), and rows just past one launch's workgroups in the other shapes.
+@pytest.mark.parametrize("rows,width,dtype", [((1 << 26) + 5, 8, torch.bfloat16),
+                                              ((1 << 20) + 3, 2056, torch.bfloat16),
+                                              ((1 << 20) + 3, 1032, torch.float32)], ids=str)
+@pytest.mark.parametrize("rms", [False, True])
+def test_more_rows_than_one_launch_takes(rows, width, dtype, rms):
+    """Equal rows far apart give equal results, and those of the oracle."""
+    say(f"[norm] {rows} rows of {width} rms={rms}")
+    n = 2053
+    few = draw(1, n, width, std=2.0, mean=0.25, dtype=dtype)
+    w, b = draw(2, width, std=0.2, mean=1.0), draw(3, width)
+    x = few.repeat((rows + n - 1) // n, 1)[:rows]
+    y, mean, rstd = qn.norm_fwd(x, w, b, rms=rms)
+    y1, mean1, rstd1 = qn.norm_fwd(few, w, b, rms=rms)   # 2053 rows: the same shape of launch
+    check(few, w, b, few, 1e-5, rms)
+    torch.cuda.synchronize()
+    for at in range(0, rows, n * 500):
+        k = min(n, rows - at)
+        assert torch.equal(y[at:at + k], y1[:k]) and torch.equal(rstd[at:at + k], rstd1[:k])
+    at = (rows - 1) // n * n
+    for a, b1 in ((y, y1), (rstd, rstd1), *(() if rms else ((mean, mean1),))):
+        assert torch.equal(a[at:], b1[:rows - at])
+        edge = (1 << 20) // n * n   # where a launch of one row per workgroup ends
+        assert torch.equal(a[edge:edge + n], b1[:min(n, rows - edge)])
