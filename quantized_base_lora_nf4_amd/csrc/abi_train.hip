@@ -32,7 +32,9 @@ int32_t attn_ok(const qlora_attention_t* a) {
   if (!aligned(a->cu_seqlens_q, 4) || !aligned(a->cu_seqlens_k, 4)) return QLORA_ERR_INVALID;
   if (a->head_dim < 1) return QLORA_ERR_INVALID;
   if (a->head_dim > QLORA_ATTN_MAX_DIM || a->head_dim % 8 != 0) return QLORA_ERR_UNSUPPORTED;
-  // every launch's workgroups (a tile has at least 32 rows) fit in 31 bits
+  // Every pass's workgroups are counted in 32 bits.  A tile has 128 rows, and
+  // attn_splits gives it at most one workgroup per 64 rows of its walk, times
+  // the heads of a group; beside more than 65536 tiles it gives it one.
   const int64_t rows = a->q_rows > a->k_rows ? a->q_rows : a->k_rows;
   const int64_t tiles = a->cu_seqlens_q ? rows / 32 + a->n_seq + 1
                                         : (rows / 32 + 1) * (a->n_seq > 0 ? a->n_seq : 1);

@@ -37,6 +37,12 @@ constexpr int kBlock = kWaves * kCols;  // columns per workgroup
 
 constexpr unsigned kResident = 512;     // workgroups that run at once: two on each of 256 CUs
 
+// Workgroups of a launch; a pass of more takes further launches.  HIP takes
+// fewer than 2^32 threads along a dimension of the grid, 2^24 workgroups of 256
+// (2^24 + 48 in one launch: most were never run, and no error came back); at
+// a quarter of that a launch lasts far longer than the next one's start takes.
+constexpr int64_t kMaxGrid = 1 << 22;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
@@ -94,9 +100,9 @@ __device__ __forceinline__ int clamp_row(int64_t v, int64_t lo, int64_t hi) {
 template <bool kKeys>
 __device__ __forceinline__ Work find_work(const AttnArgs& p, int slots, unsigned heads) {
   Work w;
-  // heads of the whole batch, times splits, is below 2^31 (the grid's size)
+  // heads of the whole batch, times splits, is below 2^32 (all workgroups are)
   const unsigned all = heads * (p.cu_q ? 1u : (unsigned)p.nseq) * (unsigned)p.splits;
-  const Place at = place_of(blockIdx.x, all);
+  const Place at = place_of(p.first + blockIdx.x, all);
   const unsigned head = at.head / (unsigned)p.splits;
   w.split = (int)(at.head - head * (unsigned)p.splits);
   const unsigned batch = head / heads;
@@ -202,6 +208,20 @@ hipError_t with_dim(int D, F&& f) {
 inline int64_t tile_slots(const AttnArgs& a, int64_t cols) {
   const int64_t n = (cols + kBlock - 1) / kBlock;
   return a.cu_q ? cols / kBlock + a.nseq + 1 : (n > 0 ? n : 1);
+}
+
+// Launches a pass of `groups` workgroups.
+template <class K>
+hipError_t launch_groups(K kern, AttnArgs a, int64_t groups, int64_t slots, hipStream_t stream) {
+  a.groups = (uint32_t)groups;
+  for (int64_t first = 0; first < groups; first += kMaxGrid) {
+    a.first = (uint32_t)first;
+    const int64_t n = groups - first < kMaxGrid ? groups - first : kMaxGrid;
+    kern<<<(unsigned)n, kWaves * 64, 0, stream>>>(a, (int)slots);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ---- tiles in LDS ----

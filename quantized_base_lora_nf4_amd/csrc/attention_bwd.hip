@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attn_bwd_dkv(AttnArgs p, int
   // Where all workgroups start at once, two to a CU, the second half goes the
   // other way: the CU with the longest of the first half gets the shortest.
   const int mid = (w.ntiles + 1) / 2;
-  const bool resident = gridDim.x <= kResident;
+  const bool resident = p.groups <= kResident;
   const int tile =
       p.causal && resident && w.tile >= mid ? w.ntiles - 1 - (w.tile - mid) : w.tile;
   const int col0 = tile * kBlock;
@@ -356,9 +356,7 @@ hipError_t launch_bwd(AttnArgs a, hipStream_t stream) {
     a.splits = attn_splits(a, kAttnDq);
     a.all = a.Sq * a.H * nb;
     const int64_t slots = tile_slots(a, a.Sq);
-    k_attn_bwd_dq<DP>
-        <<<(unsigned)(slots * a.H * nb * a.splits), kWaves * 64, 0, stream>>>(a, (int)slots);
-    e = hipGetLastError();
+    e = launch_groups(k_attn_bwd_dq<DP>, a, slots * a.H * nb * a.splits, slots, stream);
     if (e == hipSuccess && a.splits > 1)
       e = launch_attn_join_sum(a, 1, &a.dq, &a.scale, a.Sq, a.H, stream);
   }
@@ -366,9 +364,7 @@ hipError_t launch_bwd(AttnArgs a, hipStream_t stream) {
     a.splits = attn_splits(a, kAttnDkv);
     a.all = a.Sk * a.Hkv * nb;
     const int64_t slots = tile_slots(a, a.Sk);
-    k_attn_bwd_dkv<DP>
-        <<<(unsigned)(slots * a.Hkv * nb * a.splits), kWaves * 64, 0, stream>>>(a, (int)slots);
-    e = hipGetLastError();
+    e = launch_groups(k_attn_bwd_dkv<DP>, a, slots * a.Hkv * nb * a.splits, slots, stream);
     if (e == hipSuccess && a.splits > 1) {
       const AttnView out[2] = {a.dk, a.dv};
       const float mul[2] = {a.scale, 1.0f};

@@ -177,10 +177,9 @@ hipError_t launch_attn_fwd(const AttnArgs& args, float* ws, hipStream_t stream) 
   a.all = heads * a.Sq;
   a.part = ws;
   a.part_lse = ws + a.splits * heads * a.Sq * a.D;
-  const unsigned grid = (unsigned)(slots * heads * a.splits);
   const hipError_t e = with_dim(a.D, [&](auto dim) {
-    k_attn_fwd<decltype(dim)::value><<<grid, kWaves * 64, 0, stream>>>(a, (int)slots);
-    return hipGetLastError();
+    return launch_groups(k_attn_fwd<decltype(dim)::value>, a, slots * heads * a.splits, slots,
+                         stream);
   });
   return e != hipSuccess || a.splits == 1 ? e : launch_attn_join_fwd(a, stream);
 }

@@ -187,6 +187,8 @@ struct AttnArgs {
   // than one, each leaves an fp32 partial result in `part` (forward: its
   // normalized output, and its log-sum-exp in part_lse), which the join adds.
   int splits;
+  uint32_t groups;             // workgroups of the pass
+  uint32_t first;              // the first one of this launch
   int64_t all;                 // rows of all heads
   float* part;                 // [splits][all][D]
   float* part_lse;             // [splits][all]

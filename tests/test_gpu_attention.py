@@ -400,3 +400,21 @@ def test_gradients_against_differences_of_the_forward():
         sd = float(np.sqrt((r.budget[name][1] * d * d).sum()))
         say(f"    {name}: {got:.6f} against {diff:.6f}, sd {sd:.6f}")
         assert abs(got - diff) <= 4 * sd + 1e-4 * (1 + abs(diff))
+
+
+def test_more_workgroups_than_one_launch_takes():
+    """2^24 + 48 tiles, whose threads are more than one grid dimension takes
+    (2^32): equal sequences far apart give equal results, and the oracle's."""
+    say("[attention] 2^24 + 48 tiles")
+    n, batch, H, D = 4099, (1 << 20) + 3, 16, 8
+    q, do = draw(1, n, 1, H, D, std=1.5), draw(2, n, 1, H, D, std=1e-2)
+    k, v = draw(3, n, 2, H, D), draw(4, n, 2, H, D)
+    one = check_all(q, k, v, do, True)
+    q, k, v, do = (t.repeat(batch // n + 1, 1, 1, 1)[:batch] for t in (q, k, v, do))
+    o, lse = qn.attention_fwd(q, k, v)
+    many = (o, lse, *qn.attention_bwd(q, k, v, o, lse, do))
+    torch.cuda.synchronize()
+    for name, a, b in zip(("o", "lse", "dq", "dk", "dv"), many, one):
+        for at in range(0, batch, n):
+            m = min(n, batch - at)
+            assert torch.equal(a[at:at + m], b[:m]), f"{name}: sequence {at} and on"
