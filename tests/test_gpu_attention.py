@@ -418,3 +418,82 @@ def test_more_workgroups_than_one_launch_takes():
         for at in range(0, batch, n):
             m = min(n, batch - at)
             assert torch.equal(a[at:at + m], b[:m]), f"{name}: sequence {at} and on"
+
+
+# sequences, queries of a few / keys of many rows, heads, key/value heads, dim, causal.
+# 64 and more sequences are found in another way than fewer.
+MANY = [(63, False, 4, 2, 64, True), (64, False, 4, 2, 64, True), (65, False, 2, 1, 128, True),
+        (130, False, 2, 2, 64, False), (129, False, 1, 1, 80, True), (64, True, 1, 1, 128, False),
+        (131, True, 2, 1, 64, True), (700, False, 1, 1, 8, True)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
+def test_packed_with_many_sequences_of_every_length(case):
+    """Empty sequences, single rows, whole tiles, one row more, several tiles,
+    with other lengths on the side of the keys and a tail of several tiles."""
+    n, few, H, Hk, D, causal = case
+    say(f"[attention] {n} sequences {case}")
+    rng = np.random.default_rng(n)
+    some = [0, 1, 2, 31, 64, 127, 128, 129, 300, 700]
+    lk = rng.choice(some, n, p=[0.15, 0.15, 0.15, 0.15, 0.1, 0.07, 0.07, 0.07, 0.05, 0.04])
+    lk = 4 * lk if few else lk
+    lq = rng.integers(0, 5, n) if few else rng.permutation(lk)
+    lq[-1], lk[-1] = (3, 700) if few else (257, 300)   # the last one is not a trivial one
+    cq, ck = (torch.tensor(np.cumsum([0, *x]), dtype=torch.int32, device="cuda") for x in (lq, lk))
+    tail = 300
+    q, do = draw(1, sum(lq) + tail, H, D, std=1.5), draw(2, sum(lq) + tail, H, D, std=1e-2)
+    k, v = draw(3, sum(lk) + tail, Hk, D), draw(4, sum(lk) + tail, Hk, D)
+    for t in (q, do, k, v):
+        t[-tail:] = float("nan")
+    if few:
+        c = qn.train_ops._AttnCall(q, k, v, causal, None, cq, ck).c
+        assert qn.lib().qlora_attention_fwd_workspace_size(c) > 0   # walks are shared here
+    o, lse, dq, dk, dv = check_all(q, k, v, do, causal, cu=cq, cu_k=ck)
+    assert torch.isneginf(lse[:, -tail:]).all()
+    for t in (o, dq, dk, dv):
+        assert not t[-tail:].any()
+
+
+def guarded(rows, heads, dim, value, guard=float("nan"), ends=300):
+    """(rows of `value`, the buffer they lie in: `ends` rows of `guard` before
+    and after them)."""
+    buf = torch.full((rows + 2 * ends, heads, dim), guard, dtype=torch.bfloat16, device="cuda")
+    buf[ends:-ends] = value
+    return buf[ends:-ends], buf
+
+
+WRONG = {"past the end": [0, 400, 300], "negative": [-5, 100, 300], "descending": [0, 200, 100],
+         "not from zero": [250, 20, 299], "extreme": [0, 1 << 30, -(1 << 30)],
+         "limits": [-(1 << 31), (1 << 31) - 1],
+         "saw": [0, 300] * 40, "many extremes": [0, (1 << 31) - 1, -(1 << 31)] * 50,
+         "many descending": list(range(299, 0, -2)), "many past the end": list(range(0, 100000, 500))}
+
+
+@pytest.mark.parametrize("heads,kv_heads,rows", [(2, 1, 300), (1, 1, 5000)])
+@pytest.mark.parametrize("bad", WRONG, ids=lambda s: s.replace(" ", "-"))
+def test_wrong_offsets_touch_nothing_outside_the_tensors(bad, heads, kv_heads, rows):
+    """Rows around the inputs are NaN and never reach an output; rows around
+    the outputs keep what they held.  (The workspace starts as zeros: rows that
+    no sequence covers are joined from what it holds.)"""
+    say(f"[attention] guard rows, {bad}, {rows} rows")
+    D = 64
+    ins = [guarded(rows, h, D, draw(i, rows, h, D, std=0.1))[0]
+           for i, h in enumerate((heads, kv_heads, kv_heads, heads, heads))]
+    q, k, v, o, do = ins
+    outs = [guarded(rows, h, D, 5.0, 7.0) for h in (heads, heads, kv_heads, kv_heads)]
+    cu = torch.tensor(WRONG[bad], dtype=torch.int32, device="cuda")
+    good = torch.tensor(np.linspace(0, rows, len(cu)).astype(int), dtype=torch.int32, device="cuda")
+    lse = torch.zeros(heads, rows, device="cuda")
+    for cq, ck in ((cu, cu), (cu, good), (good, cu)):
+        c = qn.train_ops._AttnCall(q, k, v, True, None, cq, ck).c
+        ws = torch.zeros(max(qn.lib().qlora_attention_fwd_workspace_size(c),
+                             qn.lib().qlora_attention_bwd_workspace_size(c)),
+                         dtype=torch.uint8, device="cuda")
+        qn.attention_fwd(q, k, v, cu_seqlens=cq, cu_seqlens_k=ck, out=outs[0][0], ws=ws)
+        ws.zero_()
+        qn.attention_bwd(q, k, v, o, lse, do, cu_seqlens=cq, cu_seqlens_k=ck, ws=ws,
+                         out=tuple(t for t, _ in outs[1:]))
+        torch.cuda.synchronize()
+        for t, buf in outs:
+            assert not torch.isnan(t).any()
+            assert bool((buf[:300] == 7.0).all()) and bool((buf[-300:] == 7.0).all())
