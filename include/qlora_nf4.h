@@ -565,15 +565,15 @@ int32_t qlora_norm_bwd(const void* dy, const void* x, int64_t rows, int64_t widt
  *   grads      HOST array of n device pointers (aligned to their elements)
  *   sizes      HOST array: elements of each (0 allowed; 2^44 in all)
  *   types      HOST array: QLORA_TYPE_* of each
- *   max_norm   >= 0 (not NaN); +inf never scales
+ *   max_norm   >= 0 (not NaN); with +inf the factor is 1 unless the norm is NaN
  *   out        HOST array of n device pointers that take the scaled gradients
  *              (same sizes and types; each either its gradient itself or
  *              apart from all of them), or NULL: in place.  In place, nothing
  *              is written when the factor is 1.
  *   norm       one float (device) out, the norm before scaling
  * The three arrays are read during the call and not kept.  Squares are summed
- * in fp64.  A NaN norm scales by NaN, an infinite one by 0, as
- * min(1, max_norm / (norm + 1e-6)) says.  ws: 16-byte aligned device memory of
+ * in fp64.  A NaN norm scales by NaN, and an infinite one by 0 if max_norm is
+ * finite, as min(1, max_norm / (norm + 1e-6)) says.  ws: 16-byte aligned device memory of
  * qlora_clip_workspace_size(n) bytes.
  * qlora_grad_norm is the norm alone. */
 size_t qlora_clip_workspace_size(int64_t n);

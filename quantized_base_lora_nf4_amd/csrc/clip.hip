@@ -194,9 +194,11 @@ __global__ __launch_bounds__(kNT) void k_grad_scale(ScaleTable tb, const double*
   __shared__ double s[kNT / 64];
   const double norm = total_norm(part, slots, s);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  // a norm that is NaN gives a factor of NaN, an infinite one a factor of 0
+  // a norm that is NaN gives a factor of NaN, an infinite one a factor of 0, but
+  // 1 without a limit (inf / inf)
   const double f = (double)max_norm / (norm + 1e-6);
-  const float c = f >= 1.0 ? 1.0f : (float)f;
+  const double inf = __builtin_inf();
+  const float c = f >= 1.0 || (max_norm == inf && norm == inf) ? 1.0f : (float)f;
   if (in_place && c == 1.0f) return;
   for_chunks(tb, [&](int t, int64_t first, int count, bool f32) {
     if (f32) chunk_scale((float*)tb.out[t] + first, (const float*)tb.g[t] + first, count, c);

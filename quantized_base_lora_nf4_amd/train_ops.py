@@ -483,7 +483,8 @@ def grad_norm(grads, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Te
 def clip_grad_norm(grads, max_norm: float, out=None, ws: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:
     """Scale the gradients by min(1, max_norm / (norm + 1e-6)) and return
-    their norm before that (a one-element float32 device tensor).
+    their norm before that (a one-element float32 device tensor).  A max_norm
+    of infinity leaves them as they are, unless the norm is NaN.
 
     Each gradient is given once.  out: None scales in place; a list of tensors (one per gradient that is
     not None, same shape and dtype) takes the scaled gradients instead, and

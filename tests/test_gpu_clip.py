@@ -168,3 +168,25 @@ def test_replays_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(n, expect)
         assert all(torch.equal(a, b) for a, b in zip(g, copy))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_no_limit_leaves_infinite_gradients_alone(dtype):
+    """max_norm = inf: the same bits in place and elsewhere, though the norm is
+    infinite; a NaN norm still scales by NaN."""
+    say("[clip] no limit")
+    inf = float("inf")
+    g = [draw(1, 300, dtype=dtype), draw(2, 5, dtype=dtype)]
+    g[1][3] = -inf
+    before = [t.clone() for t in g]
+    out = [torch.zeros_like(t) for t in g]
+    for o in (out, None):
+        n = qn.clip_grad_norm(g, inf, out=o)
+        assert torch.isinf(n).all()
+        for a, b in zip(g if o is None else o, before):
+            assert torch.equal(a, b)
+    ref_norm, ref = norms.clip([host(t) for t in before], inf)
+    assert ref_norm == inf and all(np.array_equal(host(a), b) for a, b in zip(g, ref))
+    g[0][7] = float("nan")
+    n = qn.clip_grad_norm(g, inf)
+    assert torch.isnan(n).all() and all(torch.isnan(t).all() for t in g)
