@@ -30,7 +30,7 @@ def norm_backward(dy, x, weight, eps: float, rms: bool):
 def clip(grads, max_norm: float):
     """(norm, scaled gradients) of a list of arrays."""
     norm = np.sqrt(sum(float((np.asarray(g, np.float64) ** 2).sum()) for g in grads))
-    factor = max_norm / (norm + 1e-6)
     # without a limit nothing is scaled, whatever size the norm has
-    factor = 1.0 if factor >= 1.0 or (max_norm == np.inf and norm == np.inf) else factor
+    factor = 1.0 if max_norm == norm == np.inf else max_norm / (norm + 1e-6)
+    factor = 1.0 if factor >= 1.0 else factor
     return norm, [np.asarray(g, np.float64) * factor for g in grads]
