@@ -459,7 +459,9 @@ int32_t qlora_ilp_plan(int32_t n_matrices, int32_t n_configs, const double* err,
  * and element strides; the dim stride is 1.  Strides must be multiples of 8,
  * not negative, and the row stride at most QLORA_ATTN_MAX_STRIDE.  q, k and v
  * may be views of one projection's output; strides of 0 are allowed for
- * inputs.  The batch stride is not used for packed batches. */
+ * inputs.  An output's rows lie apart: from the smallest stride up, each
+ * reaches past what the dimensions before it span (else QLORA_ERR_INVALID).
+ * The batch stride is not used for packed batches. */
 #define QLORA_ATTN_MAX_STRIDE ((int64_t)1 << 22)
 typedef struct qlora_heads_t {
   uint16_t* data;
@@ -500,6 +502,8 @@ typedef struct qlora_attention_t {
  * are fp32; the probabilities are rounded to bf16 for the product with V.
  * Values outside a sequence never reach its outputs, whatever they are; a
  * NaN or infinity inside one may reach every row of that sequence and head.
+ * o may be q itself (the same view); apart from that it overlaps no input (one
+ * that starts at the same address: QLORA_ERR_INVALID).
  * ws_bytes >= qlora_attention_fwd_workspace_size(a) (16-byte aligned; 0, and
  * ws may be NULL, where the work is not split: see the backward pass). */
 size_t qlora_attention_fwd_workspace_size(const qlora_attention_t* a);
@@ -516,6 +520,9 @@ int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
  * dK and dV summed over the query heads of a key/value head.  dq, dk and dv
  * are overwritten; queries that see no key, and keys that no query sees, get
  * 0.  P and dS are rounded to bf16 for the products that follow.
+ * dq may be o itself, dk k and dv v (the same view); apart from that the
+ * outputs overlap neither each other nor an input (those that start at the same
+ * address: QLORA_ERR_INVALID).
  * ws_bytes >= qlora_attention_bwd_workspace_size(a) (16-byte aligned; 0 for
  * invalid sizes or nothing to compute).  Both calls split long walks over
  * several workgroups where that is faster (few tiles, or few key/value heads

@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "kernels.hpp"
 
 using namespace qn;
@@ -50,6 +52,34 @@ bool view_ok(const qlora_heads_t* t, int64_t rows) {
          t->head_stride >= 0 && t->batch_stride % 8 == 0 && t->row_stride % 8 == 0 &&
          t->head_stride % 8 == 0 && t->row_stride <= QLORA_ATTN_MAX_STRIDE;
 }
+
+// An output's rows lie apart: taken from the smallest stride up, each stride
+// reaches past what the dimensions before it span.
+bool rows_apart(const qlora_heads_t* t, int64_t batch, int64_t rows, int64_t heads, int64_t dim) {
+  if (batch == 0 || rows == 0) return true;
+  struct {
+    int64_t n, stride;
+  } d[3] = {{batch, t->batch_stride}, {rows, t->row_stride}, {heads, t->head_stride}};
+  std::sort(d, d + 3, [](const auto& a, const auto& b) { return a.stride < b.stride; });
+  __int128 span = dim;
+  for (const auto& x : d) {
+    if (x.n == 1) continue;
+    if (x.stride < span) return false;
+    span += (__int128)(x.n - 1) * x.stride;
+  }
+  return true;
+}
+
+// Whether output `o` starts where `t` does, unless it may be `t` itself and is.
+struct Clash {
+  int64_t batch, rows, heads;
+  bool operator()(const qlora_heads_t* o, const qlora_heads_t* t, bool itself = false) const {
+    return o->data == t->data &&
+           !(itself && (batch == 1 || o->batch_stride == t->batch_stride) &&
+             (rows == 1 || o->row_stride == t->row_stride) &&
+             (heads == 1 || o->head_stride == t->head_stride));
+  }
+};
 
 inline AttnView view(const qlora_heads_t* t) {
   return AttnView{t->data, t->batch_stride, t->row_stride, t->head_stride};
@@ -138,6 +168,12 @@ int32_t qlora_attention_fwd(const qlora_attention_t* a, const qlora_heads_t* q,
   const size_t need = (size_t)attn_fwd_workspace(r) * 4;
   if (need > 0 && (!ws || !aligned(ws, 16))) return QLORA_ERR_INVALID;
   if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  const int64_t nb = a->cu_seqlens_q ? 1 : a->n_seq;
+  if (!rows_apart(o, nb, a->q_rows, a->heads, a->head_dim)) return QLORA_ERR_INVALID;
+  // a workgroup reads its queries before it, or the join, writes their outputs
+  const Clash clash{nb, a->q_rows, a->heads};
+  if (clash(o, q, true) || (nk > 0 && (clash(o, k) || clash(o, v))))
+    return QLORA_ERR_INVALID;
   r.q = view(q);
   r.k = view(k);
   r.v = view(v);
@@ -172,6 +208,24 @@ int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
   const size_t need = (size_t)attn_bwd_workspace(r) * 4;
   if (need > 0 && (!ws || !aligned(ws, 16))) return QLORA_ERR_INVALID;
   if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  const int64_t nb = a->cu_seqlens_q ? 1 : a->n_seq;
+  if (!rows_apart(dq, nb, a->q_rows, a->heads, a->head_dim) ||
+      !rows_apart(dk, nb, a->k_rows, a->kv_heads, a->head_dim) ||
+      !rows_apart(dv, nb, a->k_rows, a->kv_heads, a->head_dim))
+    return QLORA_ERR_INVALID;
+  // q and dout are read again after dq is written; o is not, and a workgroup
+  // reads its keys and values before it, or the join, writes their gradients
+  const Clash queries{nb, a->q_rows, a->heads}, keys{nb, a->k_rows, a->kv_heads};
+  if (nq > 0 && (queries(dq, q) || queries(dq, dout) || queries(dq, o, true)))
+    return QLORA_ERR_INVALID;
+  if (nk > 0 && (keys(dk, k, true) || keys(dk, v) || keys(dv, v, true) || keys(dv, k) ||
+                 keys(dk, dv)))
+    return QLORA_ERR_INVALID;
+  if (nq > 0 && nk > 0) {
+    if (queries(dq, k) || queries(dq, v)) return QLORA_ERR_INVALID;
+    for (const qlora_heads_t* t : {dk, dv})
+      if (keys(t, q) || keys(t, dout) || keys(t, o) || keys(t, dq)) return QLORA_ERR_INVALID;
+  }
   r.q = view(q);
   r.k = view(k);
   r.v = view(v);

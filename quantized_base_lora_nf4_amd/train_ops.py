@@ -189,7 +189,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
     multiple of Hkv; D a multiple of 8 up to 128; views with strides of a
     multiple of 8 are taken as they are.  Causal: the last query of a sequence
     sees its last key.  A query that sees no key gets 0 and an lse of -inf.
-    scale defaults to 1 / sqrt(D)."""
+    scale defaults to 1 / sqrt(D).  `out` takes the output: rows that lie apart,
+    overlapping no input, or q itself."""
     c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     st, ctx = _on(c.dev, stream)
     with ctx:
@@ -214,7 +215,8 @@ def attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Te
                   ws: Optional[torch.Tensor] = None, stream=None):
     """(dq, dk, dv) for the output gradient `do`, with o and lse as
     attention_fwd returned them; the other arguments as there.  `out`: the
-    three tensors to write."""
+    three tensors to write, of rows that lie apart; they overlap neither each
+    other nor an input, but dq may be o itself, dk k and dv v."""
     c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     _same("lse", lse, c.lse_shape, (torch.float32,), c.dev)
     c.add("o", o, False)

@@ -532,3 +532,38 @@ def test_the_search_for_a_sequence_does_not_grow_with_their_number():
     for a, b in zip((got[0], *got[2:]), (ref[0], *ref[2:])):
         assert torch.equal(a, b[:, 0])
     assert packed < 8 * dense
+
+
+def test_outputs_over_inputs():
+    """Over an input that is read again, over each other and with rows on top
+    of each other they are refused; where each row is read before it is
+    written they give the same bits."""
+    say("[attention] outputs over inputs")
+    for S, H, Hk in ((200, 4, 4), (1500, 2, 2)):   # whole and shared walks
+        q, k, v, do = (draw(i, 1, S, h, 64) for i, h in ((1, H), (2, Hk), (3, Hk), (4, H)))
+        o, lse = qn.attention_fwd(q, k, v)
+        grads = qn.attention_bwd(q, k, v, o, lse, do)
+        for bad in (k, v):
+            with pytest.raises(qn.QloraError, match="invalid"):
+                qn.attention_fwd(q, k, v, out=bad)
+        new = [torch.empty_like(t) for t in (q, k, v)]
+        for at, bad in ((0, q), (0, do), (0, k), (0, v), (1, q), (1, do), (1, o), (1, v), (2, k),
+                        (2, q), (1, new[2]), (1, new[0]), (2, new[0])):
+            out = list(new)
+            out[at] = bad
+            with pytest.raises(qn.QloraError, match="invalid"):
+                qn.attention_bwd(q, k, v, o, lse, do, out=tuple(out))
+        for at in range(3):
+            flat = torch.empty_like(new[at][:, :1]).expand_as(new[at])
+            out = list(new)
+            out[at] = flat
+            with pytest.raises(qn.QloraError, match="invalid"):
+                qn.attention_bwd(q, k, v, o, lse, do, out=tuple(out))
+        with pytest.raises(qn.QloraError, match="invalid"):
+            qn.attention_fwd(q, k, v, out=new[0][:, :, :1].expand_as(q))
+        buf = q.clone()
+        o2, lse2 = qn.attention_fwd(buf, k, v, out=buf)
+        assert o2 is buf and torch.equal(buf, o) and torch.equal(lse2, lse)
+        o2, k2, v2 = o.clone(), k.clone(), v.clone()
+        for a, b in zip(qn.attention_bwd(q, k2, v2, o2, lse, do, out=(o2, k2, v2)), grads):
+            assert torch.equal(a, b)

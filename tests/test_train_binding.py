@@ -269,3 +269,34 @@ def test_clip_abi_refusals():
         assert clip(**bad) == INVALID, bad
     assert clip(types=(0, 2)) == UNSUPPORTED
     assert clip(nbytes=need - 1) == WORKSPACE
+
+
+def test_attention_abi_rejects_outputs_that_overlap():
+    """On the host: rows of an output that lie on top of each other, and
+    outputs that start where a tensor does that is read after them."""
+    L = _lib.lib()
+    far = [P << i for i in range(1, 9)]
+    dense = dict(batch_stride=4 * 12 * 64, row_stride=4 * 64, head_stride=64)
+
+    def view(i, **kw):
+        return _view(**{"data": far[i], **dense, **kw})
+
+    def bwd(**kw):
+        vs = [kw.get(n, view(i)) for i, n in enumerate(("q", "k", "v", "o", "do", "dq", "dk", "dv"))]
+        return L.qlora_attention_bwd(_attn(), *vs[:4], P, *vs[4:], P, 1 << 30, None)
+    for bad in (dict(batch_stride=0), dict(row_stride=0), dict(head_stride=0), dict(head_stride=56),
+                dict(row_stride=192), dict(batch_stride=4 * 64), dict(row_stride=64)):
+        assert _fwd(_attn(), view(0), view(1), view(2), view(3, **bad)) == INVALID, bad
+        for i, n in ((5, "dq"), (6, "dk"), (7, "dv")):
+            # 2 key/value heads of 64 fit a row stride of 192
+            if n == "dq" or bad != dict(row_stride=192):
+                assert bwd(**{n: view(i, **bad)}) == INVALID, (n, bad)
+    for i in (1, 2):
+        assert _fwd(_attn(), view(0), view(1), view(2), view(i)) == INVALID
+    assert _fwd(_attn(), view(0), view(1), view(2), view(0, row_stride=2 * 4 * 64,
+                                                         batch_stride=1 << 16)) == INVALID
+    for n, over in (("dq", (0, 1, 2, 4, 6, 7)), ("dk", (0, 2, 3, 4, 5, 7)), ("dv", (0, 1, 3, 4, 5, 6))):
+        for i in over:
+            assert bwd(**{n: view(i)}) == INVALID, (n, i)
+    for n, i in (("dq", 3), ("dk", 1), ("dv", 2)):   # the view that it may be, with other strides
+        assert bwd(**{n: view(i, batch_stride=1 << 16)}) == INVALID
