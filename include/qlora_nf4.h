@@ -491,9 +491,13 @@ typedef struct qlora_attention_t {
   int32_t head_dim;             /* a multiple of 8 up to QLORA_ATTN_MAX_DIM
                                    (others: QLORA_ERR_UNSUPPORTED) */
   int32_t causal;
-  float scale;                  /* > 0, finite */
+  float scale;                  /* QLORA_ATTN_MIN_SCALE to _MAX_SCALE */
 } qlora_attention_t;
 #define QLORA_ATTN_MAX_DIM 128
+/* 2^-100 and 2^100: the kernels also compute with 1 / scale, and with scale
+ * times log2(e), in fp32. */
+#define QLORA_ATTN_MIN_SCALE 0x1p-100f
+#define QLORA_ATTN_MAX_SCALE 0x1p+100f
 
 /* qlora_attention_fwd -- per head O = softmax(scale Q K^T) V over the keys
  * that each query sees, and lse = log sum exp(scale q k) of each row (fp32,

@@ -28,7 +28,8 @@ constexpr int64_t kMaxRows = (int64_t)1 << 30;
 int32_t attn_ok(const qlora_attention_t* a) {
   if (!a || a->n_seq < 0 || a->n_seq >= kMaxRows || a->q_rows < 0 || a->q_rows >= kMaxRows ||
       a->k_rows < 0 || a->k_rows >= kMaxRows || a->heads < 1 || a->kv_heads < 1 ||
-      a->heads % a->kv_heads != 0 || !(a->scale > 0.0f) || !isfinite(a->scale))
+      a->heads % a->kv_heads != 0 || !(a->scale >= QLORA_ATTN_MIN_SCALE) ||
+      !(a->scale <= QLORA_ATTN_MAX_SCALE))
     return QLORA_ERR_INVALID;
   if ((a->cu_seqlens_q == nullptr) != (a->cu_seqlens_k == nullptr)) return QLORA_ERR_INVALID;
   if (!aligned(a->cu_seqlens_q, 4) || !aligned(a->cu_seqlens_k, 4)) return QLORA_ERR_INVALID;

@@ -189,7 +189,7 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
     multiple of Hkv; D a multiple of 8 up to 128; views with strides of a
     multiple of 8 are taken as they are.  Causal: the last query of a sequence
     sees its last key.  A query that sees no key gets 0 and an lse of -inf.
-    scale defaults to 1 / sqrt(D).  `out` takes the output: rows that lie apart,
+    scale defaults to 1 / sqrt(D) (2^-100 to 2^100).  `out` takes the output: rows that lie apart,
     overlapping no input, or q itself."""
     c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     st, ctx = _on(c.dev, stream)

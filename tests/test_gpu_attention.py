@@ -567,3 +567,15 @@ def test_outputs_over_inputs():
         o2, k2, v2 = o.clone(), k.clone(), v.clone()
         for a, b in zip(qn.attention_bwd(q, k2, v2, o2, lse, do, out=(o2, k2, v2)), grads):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -60, 2.0 ** 60, 2.0 ** 100], ids=str)
+def test_extreme_scales(scale):
+    """Tiny: every visible key counts alike.  Huge, with queries as small: the
+    scores are those of ordinary inputs."""
+    say(f"[attention] scale {scale}")
+    q, do = draw(1, 1, 150, 2, 64, std=0.2), draw(2, 1, 150, 2, 64, std=1e-2)
+    k, v = draw(3, 1, 150, 2, 64), draw(4, 1, 150, 2, 64)
+    if scale > 1:
+        q = q * (1 / scale)
+    check_all(q, k, v, do, True, scale=scale)

@@ -300,3 +300,14 @@ def test_attention_abi_rejects_outputs_that_overlap():
             assert bwd(**{n: view(i)}) == INVALID, (n, i)
     for n, i in (("dq", 3), ("dk", 1), ("dv", 2)):   # the view that it may be, with other strides
         assert bwd(**{n: view(i, batch_stride=1 << 16)}) == INVALID
+
+
+@pytest.mark.parametrize("scale", [1e-45, 1e-39, 2.0 ** -101, 2.0 ** 101, 3e38])
+def test_attention_abi_rejects_scales_whose_inverse_leaves_fp32(scale):
+    assert _fwd(_attn(scale=scale), lse=None) == INVALID
+    assert _lib.lib().qlora_attention_bwd_workspace_size(_attn(scale=scale)) == 0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1.0, 2.0 ** 100])
+def test_attention_abi_takes_the_other_scales(scale):
+    assert _lib.lib().qlora_attention_bwd_workspace_size(_attn(scale=scale)) > 0
