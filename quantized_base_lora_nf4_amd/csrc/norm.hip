@@ -492,16 +492,17 @@ hipError_t with_fwd_shape(int64_t rows, int64_t nv, F&& f) {
 // two or more bf16 vectors per thread run faster in the smaller workgroup
 // (16384 x 1024: 32.9 -> 21.5 us; 2000 x 16384: 62 -> 49 us), two fp32
 // vectors in the larger one (2048 x 5120: 24.4 us against 28.0).
-template <class F>
-auto with_bwd_shape(int64_t nv, int type, F&& f) {
+template <class T, class F>
+auto with_bwd_shape(int64_t nv, F&& f) {
   if (nv <= 64) return f(IntC<1024>{}, IntC<64>{}, IntC<1>{});
   if (nv <= 128) return f(IntC<512>{}, IntC<64>{}, IntC<2>{});
   if (nv <= 256) return f(IntC<1024>{}, IntC<256>{}, IntC<1>{});
   if (nv <= 512) return f(IntC<1024>{}, IntC<512>{}, IntC<1>{});
   if (nv <= 1024) return f(IntC<1024>{}, IntC<1024>{}, IntC<1>{});
-  if (nv <= 2048)
-    return type == kNormF32 ? f(IntC<1024>{}, IntC<1024>{}, IntC<2>{})
-                            : f(IntC<512>{}, IntC<512>{}, IntC<4>{});
+  if (nv <= 2048) {
+    if constexpr (std::is_same<T, F32T>::value) return f(IntC<1024>{}, IntC<1024>{}, IntC<2>{});
+    else return f(IntC<512>{}, IntC<512>{}, IntC<4>{});
+  }
   if (nv <= 4096) return f(IntC<1024>{}, IntC<1024>{}, IntC<4>{});
   return f(IntC<1024>{}, IntC<1024>{}, IntC<8>{});
 }
@@ -513,8 +514,10 @@ int64_t norm_max_width(int type) {
 }
 
 int norm_bwd_groups(int64_t rows, int64_t width, int type) {
-  const int rg = with_bwd_shape(row_vecs(width, type), type, [](auto nt, auto tp, auto) {
-    return (int)decltype(nt)::value / (int)decltype(tp)::value;
+  const int rg = with_norm_type(type, [&](auto t) {
+    return with_bwd_shape<decltype(t)>(row_vecs(width, type), [](auto nt, auto tp, auto) {
+      return (int)decltype(nt)::value / (int)decltype(tp)::value;
+    });
   });
   const int64_t g = (rows + rg - 1) / rg;
   return (int)(g < kMaxGroups ? g : kMaxGroups);
@@ -554,8 +557,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   if (G > 0) {
     const hipError_t e = with_norm_type(a.x_type, [&](auto t) {
       return with_norm_type(a.w_type, [&](auto pt) {
-        return with_bwd_shape(row_vecs(a.width, a.x_type), a.x_type, [&](auto nt, auto tp, auto nv) {
-          using T = decltype(t);
+        using T = decltype(t);
+        return with_bwd_shape<T>(row_vecs(a.width, a.x_type), [&](auto nt, auto tp, auto nv) {
           using PT = decltype(pt);
           constexpr int NT = decltype(nt)::value, TPR = decltype(tp)::value,
                         NV = decltype(nv)::value;

@@ -4,6 +4,8 @@ sizes, strides, alignments and workspaces, before anything is launched."""
 
 import ctypes
 import math
+import re
+import subprocess
 
 import pytest
 import torch
@@ -311,3 +313,16 @@ def test_attention_abi_rejects_scales_whose_inverse_leaves_fp32(scale):
 @pytest.mark.parametrize("scale", [2.0 ** -100, 1.0, 2.0 ** 100])
 def test_attention_abi_takes_the_other_scales(scale):
     assert _lib.lib().qlora_attention_bwd_workspace_size(_attn(scale=scale)) > 0
+
+
+def test_only_backward_norm_kernels_that_a_call_reaches_are_built():
+    """(threads, threads per row, vectors per thread) of each row type: between
+    1025 and 2048 vectors fp32 rows take 1024 threads with two each, bf16 rows 512
+    with four, and neither has the other's kernel."""
+    names = subprocess.run(["nm", qn.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    found = re.findall(r"stub__k_norm_bwdINS0_\d(F32T|BF16T)E\w*?Li(\d+)ELi(\d+)ELi(\d+)E", names)
+    got = {(t, *map(int, n)) for t, *n in found}
+    both = {(1024, 64, 1), (512, 64, 2), (1024, 256, 1), (1024, 512, 1), (1024, 1024, 1),
+            (1024, 1024, 4), (1024, 1024, 8)}
+    assert got == ({(t, *s) for t in ("F32T", "BF16T") for s in both} |
+                   {("F32T", 1024, 1024, 2), ("BF16T", 512, 512, 4)})
