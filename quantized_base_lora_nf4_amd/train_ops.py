@@ -339,13 +339,17 @@ def norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
         dw = torch.empty_like(weight) if need_dw else None
         db = torch.empty_like(weight) if need_db else None
         L = lib()
-        need = int(L.qlora_norm_bwd_workspace_size(rows, width, _TYPES[x.dtype]))
-        ws = _scratch(need, dev, ws)
+        if need_dw or need_db:
+            need = int(L.qlora_norm_bwd_workspace_size(rows, width, _TYPES[x.dtype]))
+            ws = _scratch(need, dev, ws)
+        else:
+            ws = None   # not used
         check(L.qlora_norm_bwd(dy.data_ptr(), x.data_ptr(), rows, width, _TYPES[x.dtype],
                                weight.data_ptr(), _TYPES[weight.dtype], int(rms),
                                None if rms else mean.data_ptr(), rstd.data_ptr(),
                                *(None if t is None else t.data_ptr() for t in (dx, dw, db)),
-                               ws.data_ptr(), _bytes(ws), st), "qlora_norm_bwd")
+                               None if ws is None else ws.data_ptr(), _bytes(ws), st),
+              "qlora_norm_bwd")
     return dx, dw, db
 
 

@@ -252,3 +252,20 @@ def test_more_rows_than_one_launch_takes(rows, width, dtype, rms):
         assert torch.equal(a[at:], b1[:rows - at])
         edge = (1 << 20) // n * n   # where a launch of one row per workgroup ends
         assert torch.equal(a[edge:edge + n], b1[:min(n, rows - edge)])
+
+
+def test_frozen_parameters_take_no_workspace():
+    """dx alone: nothing but dx is allocated (the partial sums of dw and db
+    would take 16 MB here)."""
+    say("[norm] dx alone")
+    x, w = draw(1, 2048, 8192, dtype=torch.bfloat16), draw(2, 8192)
+    _, mean, rstd = qn.norm_fwd(x, w)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    dx, dw, db = qn.norm_bwd(x, x, w, mean, rstd, need_dw=False, need_db=False)
+    torch.cuda.synchronize()
+    assert dw is None and db is None
+    assert torch.cuda.max_memory_allocated() - before <= dx.numel() * 2 + (1 << 20)
+    assert torch.equal(dx, qn.norm_bwd(x, x, w, mean, rstd)[0])
