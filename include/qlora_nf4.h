@@ -476,7 +476,8 @@ typedef struct qlora_heads_t {
  *   both given, equal pointers for self-attention): sequence s has the query
  *   rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1 and likewise the keys.
  *   Sequences may be empty on either side.  Rows past the last offset belong
- *   to no sequence: they are not read, and outputs there are 0 (lse -inf).
+ *   to no sequence: what they hold reaches no output, and outputs there are 0
+ *   (lse -inf).
  *   The offsets are read by the kernels and clamped to the rows, so wrong
  *   ones give undefined outputs but no access outside the tensors.
  *   Causal: query i of a sequence of lq queries and lk keys sees the keys
