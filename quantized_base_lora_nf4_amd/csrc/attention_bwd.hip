@@ -26,9 +26,9 @@
 // reloads that wait for the next tile: 1446 to 2100 us instead of 1000.)
 //
 // Measured (one sequence of 8192 tokens, 32 heads over 8 key/value heads of
-// 128, causal): dQ 687 us, dK/dV 998 us and 25 us to join its two shares;
-// 1716 us in all, 1120 TFLOP/s over the seven products against 1280 to 1390 of
-// large library products; MFMA pipes busy 59 to 63 % of the cycles at the 1.8 GHz
+// 128, causal): dQ 687 us, dK/dV 998 us and 25 us to join its two shares; the
+// call takes 1716 to 1763 us by the card, 1090 to 1120 TFLOP/s over the seven
+// products against 1280 to 1390 of large library products; MFMA pipes busy 59 to 63 % of the cycles at the 1.8 GHz
 // that the chip holds, so the clock (power) bounds them.  8 x 512 tokens,
 // 32 heads: 54 and 66 us; their loads and stores alone take 43 and 41 us.
 #include <utility>

@@ -20,10 +20,10 @@
 // wave's.
 //
 // Measured (one sequence of 8192 tokens, 32 heads over 8 key/value heads of
-// 128, causal): 513 us, 1070 TFLOP/s against 1280 to 1390 of large bf16
-// library products on the same card; the MFMA pipes are busy 52 % of the
-// cycles at the 1.84 GHz that the chip holds.  8 x 512 tokens, 32 heads: 40 us;
-// the tile loads alone, without the arithmetic, take 30 us (135 MB).
+// 128, causal): 513 to 533 us by the card, 1030 to 1070 TFLOP/s against 1280 to
+// 1390 of large bf16 library products; the MFMA pipes are busy 52 % of the
+// cycles at the 1.84 GHz that the chip holds.  8 x 512 tokens, 32 heads: 40 to
+// 42 us; the tile loads alone, without the arithmetic, take 30 us (135 MB).
 #include "attention.hpp"
 
 namespace qn {

@@ -18,6 +18,12 @@
 // loads and stores 16 bytes at any element address, so those rows take the
 // same path, with the one partial vector at the end element by element.
 //
+// The backward pass of rows of more than 2048 bf16 or 4096 fp32 vectors does
+// not fit the registers: its workgroups of 1024 threads have 128 each, and 56 to
+// 105 (four bf16 vectors per thread), 365 to 640 (eight) or 96 to 141 (eight fp32
+// vectors) are kept in scratch memory and move with every row (512 x 32768 bf16
+// rms 47 us where the bytes take 20, 512 x 65536 328 where they take 39).
+//
 // Measured: forward 4096 x 4096 bf16 13.8 us (4.9 TB/s, a large copy reaches
 // 5.1 to 5.2); backward 8192 x 8192 bf16 (rms) 76 us (5.3 TB/s), 2047 x 5120
 // fp32 31 us, of which 24 are the main kernel's (5.3 TB/s) and 4 the parameters'.
@@ -230,8 +236,9 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_norm_fwd(
 // (few rows) writes dw and db itself.  The next row's loads run during the
 // current one.
 //
-// Few, large workgroups keep the partial rows few: at 256 of them their
-// traffic is 2 % of the pass at 8192 x 8192 and 12 % at 4096 x 1024 (bf16).
+// Few, large workgroups keep the partial rows few: 256 of them, written once
+// and read once, add 4 % to the pass's bytes at 8192 x 8192 (bf16, dw alone) and
+// 17 % at 4096 x 1024 (dw and db).
 template <class T, class PT, int NT, int TPR, int NV, bool kRms, bool kBias>
 __global__ __launch_bounds__(NT) void k_norm_bwd(
     const typename T::elem* __restrict__ dy, const typename T::elem* __restrict__ x, int64_t rows,
