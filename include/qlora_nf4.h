@@ -447,7 +447,7 @@ int32_t qlora_ilp_plan(int32_t n_matrices, int32_t n_configs, const double* err,
                        const int64_t* bytes, int64_t budget, int32_t* choice,
                        double* total_err, int64_t* total_bytes);
 
-/* ---- Around the layer: attention, norms, gradient clipping ----
+/* ---- Around the layer: attention, rotary positions, norms, gradient clipping, AdamW ----
  *
  * The other operators of a finetuning step.  Element types of the norms and
  * of the clipping: QLORA_TYPE_BF16 or QLORA_TYPE_FP32 (others give
@@ -541,6 +541,47 @@ int32_t qlora_attention_bwd(const qlora_attention_t* a, const qlora_heads_t* q,
                             const qlora_heads_t* dk, const qlora_heads_t* dv, void* ws,
                             size_t ws_bytes, hipStream_t stream);
 
+/* qlora_rope -- rotary positions of q and k, in one call.  The first `rot`
+ * elements of every head turn in pairs: pair j of a row at position p by the
+ * angle a = p inv_freq[j],
+ *   (x, y) -> scale (x cos a - y sin a, y cos a + x sin a),
+ * x and y being the elements j and rot / 2 + j (interleaved = 0) or 2j and
+ * 2j + 1 (interleaved = 1).  The other elements are copied.  inverse = 1 turns
+ * by -a, which is the backward pass: the gradients of q and k from those of the
+ * outputs.  Angles are taken in fp64 (any position up to 2^40 in magnitude, also
+ * negative ones), the rotation in fp32, rounded once to bf16.
+ *   n_seq, rows   dense (cu_seqlens NULL): a batch of n_seq sequences of `rows`
+ *                 rows; packed: `rows` rows in n_seq sequences with the offsets
+ *                 cu_seqlens as in qlora_attention_t (device, int32, n_seq + 1)
+ *   positions     device, int32 or int64 by position_bytes (4, 8), with element
+ *                 strides over the batch (dense) and the rows (0 allowed); NULL:
+ *                 a row's place in its sequence, from 0.  Given positions go
+ *                 before cu_seqlens.
+ *   inv_freq      device, rot / 2 doubles
+ *   q, k          [batch, row, head, dim] views (head_dim a multiple of 8 up to
+ *                 QLORA_ROPE_MAX_DIM; 2 <= rot <= head_dim, even); k_heads = 0: q
+ *                 alone (k and k_out are not looked at)
+ *   q_out, k_out  outputs whose rows lie apart; q_out may be q itself and k_out k
+ *                 (the same view: in place); apart from that outputs overlap
+ *                 neither inputs nor each other (those that start at the same
+ *                 address: QLORA_ERR_INVALID)
+ * Rows past the last offset belong to no sequence and are copied; wrong offsets
+ * give wrong positions but no access outside the tensors. */
+#define QLORA_ROPE_MAX_DIM 1024
+typedef struct qlora_rope_t {
+  int64_t n_seq, rows;
+  const int32_t* cu_seqlens;
+  const void* positions;
+  int64_t position_batch_stride, position_row_stride;
+  const double* inv_freq;
+  int32_t position_bytes;
+  int32_t q_heads, k_heads, head_dim, rot;
+  int32_t interleaved, inverse;
+  float scale;                  /* finite */
+} qlora_rope_t;
+int32_t qlora_rope(const qlora_rope_t* a, const qlora_heads_t* q, const qlora_heads_t* k,
+                   const qlora_heads_t* q_out, const qlora_heads_t* k_out, hipStream_t stream);
+
 /* qlora_norm_fwd -- layer norm (rms = 0) or root-mean-square norm (rms = 1) of
  * each row of x [rows, width]:
  *   mean = sum(x) / width (0 if rms),  rstd = 1 / sqrt(sum((x - mean)^2) / width + eps),
@@ -595,6 +636,78 @@ int32_t qlora_clip_grad_norm(int64_t n, const void* const* grads, const int64_t*
 int32_t qlora_grad_norm(int64_t n, const void* const* grads, const int64_t* sizes,
                         const int32_t* types, float* norm, void* ws, size_t ws_bytes,
                         hipStream_t stream);
+
+/* qlora_adamw_step -- one AdamW step of n parameter tensors:
+ *   g = c grad,  c = min(1, max_norm / (norm + 1e-6)) as in qlora_clip_grad_norm
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, p rounded once to its type.
+ *   n            tensors, 0 <= n <= 2^20
+ *   params       HOST array of n device pointers (aligned to their elements; each
+ *                tensor once), updated in place
+ *   grads        HOST array: the gradients; NULL leaves that tensor and its
+ *                states alone
+ *   copies       HOST array of bf16 tensors that take the updated parameters,
+ *                rounded (for parameters held in fp32 beside a bf16 copy; NULL
+ *                entries: none), or NULL
+ *   sizes        HOST array: elements of each (0 allowed)
+ *   param_types, grad_types   HOST arrays: QLORA_TYPE_* of each
+ *   state_bits   32: m and v are fp32; 8: m is int8, v uint8, with scales below
+ *   m, v         the states of all tensors one after the other, each from a
+ *                multiple of QLORA_ADAMW_BLOCK elements on: QLORA_ADAMW_BLOCK
+ *                state_blocks elements (16-byte aligned).  A new state is all
+ *                zeros (scales too).
+ *   m_scale, v_scale   8 bits: one float per block of QLORA_ADAMW_BLOCK elements
+ *                (the last block of a tensor may be shorter); 32 bits: not used
+ *   state_blocks >= qlora_adamw_blocks(n, sizes) (else QLORA_ERR_WORKSPACE)
+ *   step         >= 1, the number of this step; lr, eps, weight_decay >= 0,
+ *                0 <= beta < 1
+ *   lr_dev, step_dev   one float, one int64 on the device that are read by the
+ *                kernels in place of lr and step (a captured step replays with
+ *                their values at that time), or NULL
+ *   norm         one float (device), the gradients' norm; NULL: no clipping
+ *   max_norm     >= 0 (not NaN), with norm
+ * The host arrays are read during the call and not kept.
+ * 8-bit states: codes with a scale s per block, the block's largest |m| and v,
+ *   m = s c |c| / 127^2,  c in -127..127;   v = s (c / 255)^4,  c in 0..255.
+ * c is the number of thresholds (i - 1/2)^2, i = 1..127, up to fl(|m| fl(127^2 / s))
+ * with the sign of m, and of ((i - 1/2)^2)^2, i = 1..255, up to fl(v fl(255^4 / s)),
+ * at least 1 where v > 0.  Blocks whose largest value is below 2^-96 get s = 0.
+ * A block with an infinity or NaN gets s = NaN: it is NaN from then on.  Products
+ * and sums up to the codes are rounded one by one to fp32, in the order written. */
+#define QLORA_ADAMW_BLOCK 256
+typedef struct qlora_adamw_t {
+  int64_t n;
+  void* const* params;
+  const void* const* grads;
+  uint16_t* const* copies;
+  const int64_t* sizes;
+  const int32_t* param_types;
+  const int32_t* grad_types;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t state_blocks;
+  int64_t step;
+  double lr, beta1, beta2, weight_decay;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* norm;
+  float eps, max_norm;
+  int32_t state_bits;
+} qlora_adamw_t;
+/* Blocks of states of n tensors; -1 for invalid sizes (2^31 blocks or more). */
+int64_t qlora_adamw_blocks(int64_t n, const int64_t* sizes);
+int32_t qlora_adamw_step(const qlora_adamw_t* a, hipStream_t stream);
+
+/* qlora_adamw_values -- the values that 8-bit states stand for, in fp32 (for
+ * inspection and conversion): m_out, v_out [blocks QLORA_ADAMW_BLOCK], 16-byte
+ * aligned, from m, v, m_scale, v_scale as above. */
+int32_t qlora_adamw_values(const void* m, const void* v, const float* m_scale,
+                           const float* v_scale, int64_t blocks, float* m_out, float* v_out,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }

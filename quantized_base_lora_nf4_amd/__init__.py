@@ -10,5 +10,7 @@ from .ops import (LqResult, NF4Weight, QLoRALinear, QLoRALinearFunction, alloc_n
                   code_table, ilp_plan, lq_init, lq_workspace_size, nf4_dequantize,
                   nf4_quantize, qlora_linear_bwd, qlora_linear_fwd, qlora_linear_fwd_noalloc,
                   quant_error, storage_bytes, user_table, workspace_size, USER_CODES)
+from .optim import AdamW, AdamWState, adamw_init, adamw_step, adamw_values  # noqa: F401
 from .train_ops import (LayerNorm, RMSNorm, attention, attention_bwd, attention_fwd,  # noqa: F401
-                        clip_grad_norm, grad_norm, norm, norm_bwd, norm_fwd)
+                        clip_grad_norm, grad_norm, norm, norm_bwd, norm_fwd, rope, rope_bwd,
+                        rope_fwd, rope_frequencies)

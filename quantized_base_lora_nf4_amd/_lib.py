@@ -34,6 +34,9 @@ QLORA_STREAM_GRID = 1024
 QLORA_TYPE_BF16 = 0
 QLORA_TYPE_FP32 = 1
 
+# Elements of a tensor per block of its 8-bit optimizer states
+QLORA_ADAMW_BLOCK = 256
+
 # Every symbol the header declares.
 EXPORTS = (
     "qlora_status_str",
@@ -71,6 +74,10 @@ EXPORTS = (
     "qlora_clip_workspace_size",
     "qlora_clip_grad_norm",
     "qlora_grad_norm",
+    "qlora_rope",
+    "qlora_adamw_blocks",
+    "qlora_adamw_step",
+    "qlora_adamw_values",
 )
 
 
@@ -112,6 +119,56 @@ class Attention(ctypes.Structure):
         ("head_dim", ctypes.c_int32),
         ("causal", ctypes.c_int32),
         ("scale", ctypes.c_float),
+    ]
+
+
+class Rope(ctypes.Structure):
+    """Mirror of qlora_rope_t."""
+    _fields_ = [
+        ("n_seq", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("position_batch_stride", ctypes.c_int64),
+        ("position_row_stride", ctypes.c_int64),
+        ("inv_freq", ctypes.c_void_p),
+        ("position_bytes", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("k_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rot", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("inverse", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class AdamW(ctypes.Structure):
+    """Mirror of qlora_adamw_t."""
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("params", ctypes.c_void_p),
+        ("grads", ctypes.c_void_p),
+        ("copies", ctypes.c_void_p),
+        ("sizes", ctypes.c_void_p),
+        ("param_types", ctypes.c_void_p),
+        ("grad_types", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("state_blocks", ctypes.c_int64),
+        ("step", ctypes.c_int64),
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("lr_dev", ctypes.c_void_p),
+        ("step_dev", ctypes.c_void_p),
+        ("norm", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("max_norm", ctypes.c_float),
+        ("state_bits", ctypes.c_int32),
     ]
 
 
@@ -210,6 +267,14 @@ def lib() -> ctypes.CDLL:
     L.qlora_clip_grad_norm.argtypes = [i64, vp, vp, vp, f32, vp, vp, vp, sz, vp]
     L.qlora_grad_norm.restype = i32
     L.qlora_grad_norm.argtypes = [i64, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_rope.restype = i32
+    L.qlora_rope.argtypes = [ctypes.POINTER(Rope), ph, ph, ph, ph, vp]
+    L.qlora_adamw_blocks.restype = i64
+    L.qlora_adamw_blocks.argtypes = [i64, vp]
+    L.qlora_adamw_step.restype = i32
+    L.qlora_adamw_step.argtypes = [ctypes.POINTER(AdamW), vp]
+    L.qlora_adamw_values.restype = i32
+    L.qlora_adamw_values.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp]
     _lib = L
     return L
 

@@ -1,5 +1,5 @@
-// C ABI of the operators around the layer (attention, norms, gradient
-// clipping): argument checks and workspaces.  The declarations, with the
+// C ABI of the operators around the layer (attention, rotary positions, norms,
+// gradient clipping, AdamW): argument checks and workspaces.  The declarations, with the
 // meaning of every argument, are in include/qlora_nf4.h.
 #include "../../include/qlora_nf4.h"
 
@@ -304,6 +304,147 @@ int32_t qlora_grad_norm(int64_t n, const void* const* grads, const int64_t* size
                         const int32_t* types, float* norm, void* ws, size_t ws_bytes,
                         hipStream_t stream) {
   return clip(n, grads, sizes, types, false, 0.0f, nullptr, norm, ws, ws_bytes, stream);
+}
+
+int32_t qlora_rope(const qlora_rope_t* a, const qlora_heads_t* q, const qlora_heads_t* k,
+                   const qlora_heads_t* q_out, const qlora_heads_t* k_out, hipStream_t stream) {
+  if (!a || a->n_seq < 0 || a->n_seq >= kMaxRows || a->rows < 0 || a->rows >= kMaxRows ||
+      a->q_heads < 1 || a->k_heads < 0 || a->q_heads > (1 << 20) || a->k_heads > (1 << 20) ||
+      a->head_dim < 1 || a->rot < 2 || a->rot % 2 != 0 || a->rot > a->head_dim ||
+      !isfinite(a->scale))
+    return QLORA_ERR_INVALID;
+  if (a->head_dim > QLORA_ROPE_MAX_DIM || a->head_dim % 8 != 0) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned(a->cu_seqlens, 4)) return QLORA_ERR_INVALID;
+  if (a->positions &&
+      ((a->position_bytes != 4 && a->position_bytes != 8) ||
+       !aligned(a->positions, a->position_bytes) || a->position_batch_stride < 0 ||
+       a->position_row_stride < 0))
+    return QLORA_ERR_INVALID;
+  const int64_t nb = a->cu_seqlens ? 1 : a->n_seq;
+  const int64_t tokens = nb * a->rows;
+  const bool keys = a->k_heads > 0;
+  if (!view_ok(q, tokens) || !view_ok(q_out, tokens) ||
+      (keys && (!view_ok(k, tokens) || !view_ok(k_out, tokens))))
+    return QLORA_ERR_INVALID;
+  if (tokens == 0) return QLORA_OK;
+  if (!a->inv_freq || !aligned(a->inv_freq, 8)) return QLORA_ERR_INVALID;
+  if (!rows_apart(q_out, nb, a->rows, a->q_heads, a->head_dim) ||
+      (keys && !rows_apart(k_out, nb, a->rows, a->k_heads, a->head_dim)))
+    return QLORA_ERR_INVALID;
+  const Clash qs{nb, a->rows, a->q_heads}, ks{nb, a->rows, a->k_heads};
+  if (qs(q_out, q, true)) return QLORA_ERR_INVALID;
+  if (keys && (ks(k_out, k, true) || qs(q_out, k) || ks(k_out, q) || qs(q_out, k_out)))
+    return QLORA_ERR_INVALID;
+  RopeArgs r{};
+  r.q = view(q);
+  r.qo = view(q_out);
+  if (keys) {
+    r.k = view(k);
+    r.ko = view(k_out);
+  }
+  r.tokens = tokens;
+  r.rows = a->rows;
+  r.cu = a->positions ? nullptr : a->cu_seqlens;
+  r.nseq = (int)a->n_seq;
+  r.pos = a->positions;
+  r.pos_sb = a->position_batch_stride;
+  r.pos_st = a->position_row_stride;
+  r.pos64 = a->position_bytes == 8;
+  r.freq = a->inv_freq;
+  r.H = a->q_heads;
+  r.Hk = a->k_heads;
+  r.D = a->head_dim;
+  r.rot = a->rot;
+  r.interleaved = a->interleaved != 0;
+  r.inverse = a->inverse != 0;
+  r.scale = a->scale;
+  return launch_status(launch_rope(r, stream));
+}
+
+static_assert(kAdamBlock == QLORA_ADAMW_BLOCK, "block of the optimizer's states");
+
+int64_t qlora_adamw_blocks(int64_t n, const int64_t* sizes) {
+  if (n < 0 || n > kMaxTensors || (n > 0 && !sizes)) return -1;
+  const int64_t most = ((int64_t)1 << 31) - 1;
+  int64_t blocks = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (sizes[i] < 0 || sizes[i] > most * kAdamBlock) return -1;
+    blocks += (sizes[i] + kAdamBlock - 1) / kAdamBlock;
+    if (blocks > most) return -1;
+  }
+  return blocks;
+}
+
+int32_t qlora_adamw_step(const qlora_adamw_t* a, hipStream_t stream) {
+  if (!a) return QLORA_ERR_INVALID;
+  if (a->state_bits != 8 && a->state_bits != 32) return QLORA_ERR_UNSUPPORTED;
+  const int64_t blocks = qlora_adamw_blocks(a->n, a->sizes);
+  if (blocks < 0) return QLORA_ERR_INVALID;
+  const auto beta_ok = [](double b) { return b >= 0.0 && b < 1.0; };
+  const auto rate_ok = [](double x) { return x >= 0.0 && isfinite(x); };
+  if ((a->step < 1 && !a->step_dev) || !rate_ok(a->lr) || !beta_ok(a->beta1) ||
+      !beta_ok(a->beta2) || !rate_ok(a->weight_decay) || !rate_ok(a->eps) ||
+      (a->norm && !(a->max_norm >= 0.0f)))
+    return QLORA_ERR_INVALID;
+  if (!aligned(a->lr_dev, 4) || !aligned(a->step_dev, 8) || !aligned(a->norm, 4))
+    return QLORA_ERR_INVALID;
+  if (a->n > 0 && (!a->params || !a->grads || !a->param_types || !a->grad_types))
+    return QLORA_ERR_INVALID;
+  for (int64_t i = 0; i < a->n; ++i) {
+    if (!type_ok(a->param_types[i]) || !type_ok(a->grad_types[i])) return QLORA_ERR_UNSUPPORTED;
+    if (a->sizes[i] == 0 || !a->grads[i]) continue;
+    if (!a->params[i] || !aligned(a->params[i], type_bytes(a->param_types[i])) ||
+        !aligned(a->grads[i], type_bytes(a->grad_types[i])))
+      return QLORA_ERR_INVALID;
+    if (a->copies && !aligned(a->copies[i], 2)) return QLORA_ERR_INVALID;
+  }
+  if (blocks == 0) return QLORA_OK;
+  if (!a->m || !a->v || !aligned(a->m, 16) || !aligned(a->v, 16)) return QLORA_ERR_INVALID;
+  if (a->state_bits == 8 &&
+      (!a->m_scale || !a->v_scale || !aligned(a->m_scale, 4) || !aligned(a->v_scale, 4)))
+    return QLORA_ERR_INVALID;
+  if (a->state_blocks < blocks) return QLORA_ERR_WORKSPACE;
+  AdamArgs r{};
+  r.n = a->n;
+  r.params = a->params;
+  r.grads = a->grads;
+  r.copies = a->copies;
+  r.sizes = a->sizes;
+  r.p_types = a->param_types;
+  r.g_types = a->grad_types;
+  r.bits = a->state_bits;
+  r.m = a->m;
+  r.v = a->v;
+  r.ms = a->m_scale;
+  r.vs = a->v_scale;
+  AdamHyper& h = r.hyper;
+  h.lr = a->lr;
+  h.beta1 = a->beta1;
+  h.beta2 = a->beta2;
+  h.decay = a->weight_decay;
+  if (!a->step_dev) {
+    h.bc1 = 1.0 - pow(a->beta1, (double)a->step);
+    h.bc2 = 1.0 - pow(a->beta2, (double)a->step);
+  }
+  h.log_beta1 = log(a->beta1);
+  h.log_beta2 = log(a->beta2);
+  h.lr_dev = a->lr_dev;
+  h.step_dev = a->step_dev;
+  h.norm = a->norm;
+  h.max_norm = a->max_norm;
+  h.eps = a->eps;
+  return launch_status(launch_adamw(r, stream));
+}
+
+int32_t qlora_adamw_values(const void* m, const void* v, const float* m_scale,
+                           const float* v_scale, int64_t blocks, float* m_out, float* v_out,
+                           hipStream_t stream) {
+  if (blocks < 0 || blocks >= (int64_t)1 << 31) return QLORA_ERR_INVALID;
+  if (blocks == 0) return QLORA_OK;
+  if (!m || !v || !m_scale || !v_scale || !m_out || !v_out || !aligned(m, 16) || !aligned(v, 16) ||
+      !aligned(m_scale, 4) || !aligned(v_scale, 4) || !aligned(m_out, 16) || !aligned(v_out, 16))
+    return QLORA_ERR_INVALID;
+  return launch_status(launch_adamw_values(m, v, m_scale, v_scale, blocks, m_out, v_out, stream));
 }
 
 }  // extern "C"

@@ -163,6 +163,37 @@ struct ClipArgs {
 };
 hipError_t launch_clip(const ClipArgs& a, hipStream_t stream);
 
+// ---- adamw.hip: the AdamW step over many tensors ----
+constexpr int kAdamBlock = 256;   // elements of a tensor per block of its 8-bit states
+constexpr int kAdamGrid = 2048;   // workgroups per launch at most
+struct AdamHyper {
+  double lr, beta1, beta2, decay;
+  double bc1, bc2;               // 1 - beta^t (host's, unless step_dev)
+  double log_beta1, log_beta2;   // for step_dev
+  const float* lr_dev;           // device scalars, or null
+  const int64_t* step_dev;
+  const float* norm;             // the gradients' norm, or null: no clipping
+  float max_norm, eps;
+};
+struct AdamArgs {
+  int64_t n;
+  void* const* params;           // host arrays of device pointers
+  const void* const* grads;      // null: the tensor is left alone
+  uint16_t* const* copies;       // bf16 copies of the parameters (entries may be null), or null
+  const int64_t* sizes;
+  const int32_t* p_types;        // kNormBF16 / kNormF32
+  const int32_t* g_types;
+  int bits;                      // of the states: 32 (fp32) or 8 (int8 m, uint8 v)
+  void* m;                       // every tensor's states from a multiple of kAdamBlock on
+  void* v;
+  float* ms;                     // scales, one per block (8 bits)
+  float* vs;
+  AdamHyper hyper;
+};
+hipError_t launch_adamw(const AdamArgs& a, hipStream_t stream);
+hipError_t launch_adamw_values(const void* m, const void* v, const float* ms, const float* vs,
+                               int64_t blocks, float* m_out, float* v_out, hipStream_t stream);
+
 // ---- attention_fwd.hip, attention_bwd.hip, attention_join.hip ----
 // A [batch, token, head, dim] tensor: element strides (the last one is 1).
 struct AttnView {
@@ -208,6 +239,22 @@ hipError_t launch_attn_bwd(const AttnArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_attn_join_fwd(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_join_sum(const AttnArgs& a, int n, const AttnView* out, const float* mul,
                                 int64_t rows, int heads, hipStream_t stream);
+
+// ---- rope.hip: rotary positions ----
+struct RopeArgs {
+  AttnView q, k, qo, ko;     // inputs and outputs (k, ko: unused if Hk == 0)
+  int64_t tokens, rows;      // tokens in all; per batch entry (packed: all)
+  const int32_t* cu;         // packed: sequence offsets, or null
+  int nseq;
+  const void* pos;           // positions, or null: a row's place in its sequence
+  int64_t pos_sb, pos_st;    // element strides over the batch and the rows
+  bool pos64;                // int64 positions (else int32)
+  const double* freq;        // [rot / 2] radians per position
+  int H, Hk, D, rot;
+  bool interleaved, inverse;
+  float scale;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 
 // ---- stream.hip: read-only HBM stream (measurement helper) ----
 // Reads bytes / 16 16-byte words of src with `grid` workgroups of 256

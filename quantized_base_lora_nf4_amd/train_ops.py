@@ -1,5 +1,6 @@
-"""Thin torch binding of the operators around the layer: attention, layer and
-root-mean-square norms, and the clipping of gradients by their global norm.
+"""Thin torch binding of the operators around the layer: attention, rotary
+positions, layer and root-mean-square norms, and the clipping of gradients by
+their global norm.
 
 As in :mod:`quantized_base_lora_nf4_amd.ops`: argument checks and marshalling
 only, every call enqueues on ``torch.cuda.current_stream()`` of the tensors'
@@ -17,7 +18,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, check, lib
+from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Rope, check, lib
 from .ops import _stream_obj
 
 _SIXTEEN = (torch.bfloat16, torch.int16, torch.uint16)
@@ -266,6 +267,189 @@ def attention(q, k, v, causal: bool = True, scale: Optional[float] = None, cu_se
     """attention_fwd with gradients for q, k and v (torch autograd); returns
     the output only."""
     return _AttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+
+def rope_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                     factor: float = 1.0, length: int = 4096, low: float = 1.0,
+                     high: float = 32.0, device="cuda"):
+    """(inv_freq, scale) for the rotation of `dim` elements of a head: dim / 2
+    radians per position (float64, on `device`) and the factor of the rotated
+    values, as rope_fwd takes them.
+
+    scaling, for contexts `factor` times longer than the trained `length`:
+      None      base^(-2 j / dim)
+      "linear"  all of them divided by factor (positions interpolated)
+      "base"    base times factor^(dim / (dim - 2)): the slowest pair is
+                interpolated, the fastest stays
+      "parts"   pairs of more than `high` turns within `length` stay, those of
+                less than `low` are divided by factor, and between, the share
+                that stays grows linearly with the number of turns; scale =
+                0.1 ln(factor) + 1
+      "bands"   the same ramp, and scale 1 (`high` is commonly 4 here)."""
+    if dim < 2 or dim % 2:
+        raise ValueError(f"dim must be even and at least 2, got {dim}")
+    if not (base > 0 and factor >= 1.0 and length >= 1):
+        raise ValueError("base must be positive, factor at least 1, length at least 1")
+    if scaling == "base":
+        if dim < 4:
+            raise ValueError("scaling 'base' needs 4 elements at least")
+        base *= factor ** (dim / (dim - 2))
+    f = base ** -(torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("parts", "bands"):
+        if not high > low:
+            raise ValueError(f"high ({high}) must be above low ({low})")
+        stay = ((length * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * stay + f / factor * (1.0 - stay)
+        if scaling == "parts" and factor > 1.0:
+            scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"scaling must be None, 'linear', 'base', 'parts' or 'bands', "
+                         f"got {scaling!r}")
+    return f.to(device), scale
+
+
+def _rope_call(names, q, k, inv_freq, positions, cu_seqlens, interleaved, scale, out, inverse,
+               stream):
+    qn, kn = names
+    dev = _device_of(qn, q)
+    qs = q.shape
+    if len(qs) not in (3, 4):
+        raise ValueError(f"{qn} must have 4 dimensions [batch, row, head, dim], or 3 [row, head, dim]")
+    packed = len(qs) == 3
+    if cu_seqlens is not None and not packed:
+        raise ValueError(f"cu_seqlens needs a packed {qn} of 3 dimensions")
+    heads, dim = qs[-2], qs[-1]
+    rows = qs[-3]
+    kv = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != len(qs):
+            raise ValueError(f"{kn} must have {len(qs)} dimensions, as {qn}")
+        kv = k.shape[-2]
+        if kv < 1:
+            raise ValueError(f"{kn} has no heads")
+    if heads < 1:
+        raise ValueError(f"{qn} has no heads")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a 1-D tensor")
+    _same("inv_freq", inv_freq, inv_freq.shape, (torch.float64,), dev)
+    rot = 2 * inv_freq.numel()
+    if not 2 <= rot <= dim:
+        raise ValueError(f"inv_freq has {rot // 2} elements: heads of {dim} take 1 to {dim // 2}")
+    pos = cu = None
+    psb = pst = pbytes = 0
+    nseq = 1 if packed else qs[0]
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a torch tensor")
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions has dtype {positions.dtype}, expected torch.int32 or torch.int64")
+        shape = qs[:-2]
+        if positions.shape != shape and (packed or positions.shape not in ((rows,), (1, rows))):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {tuple(shape)}"
+                             f"{'' if packed else f' or ({rows},)'}")
+        if positions.device != dev:
+            raise ValueError(f"positions is on {positions.device}, expected {dev}")
+        pos, pbytes = positions.data_ptr(), positions.element_size()
+        pst = positions.stride(-1)
+        if positions.dim() == 2 and positions.shape[0] == nseq and nseq > 1:
+            psb = positions.stride(0)
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a 1-D tensor of offsets")
+        _same("cu_seqlens", cu_seqlens, cu_seqlens.shape, (torch.int32,), dev)
+        cu, nseq = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+    kshape = (*qs[:-2], kv, dim)
+    words = [*_heads(qn, q, qs, dev, packed)]
+    words += _heads(kn, k, kshape, dev, packed) if kv else (0, 0, 0, 0)
+    st, ctx = _on(dev, stream)
+    with ctx:
+        if out is None:
+            # (as _AttnCall.new)
+            qo = torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+            words += (qo.data_ptr(), 0 if packed else rows * heads * dim, heads * dim, dim)
+            ko = None
+            if kv:
+                ko = torch.empty_like(k, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+                words += (ko.data_ptr(), 0 if packed else rows * kv * dim, kv * dim, dim)
+        else:
+            qo, ko = out
+            words += _heads("out[0]", qo, qs, dev, packed)
+            if kv:
+                words += _heads("out[1]", ko, kshape, dev, packed)
+        if not kv:
+            words += (0, 0, 0, 0)
+        a = array.array("q", words)
+        base = a.buffer_info()[0]
+        check(lib().qlora_rope(Rope(nseq, rows, cu, pos, psb, pst, inv_freq.data_ptr(), pbytes, heads,
+                                    kv, dim, rot, int(interleaved), inverse, float(scale)),
+                               base, base + 32, base + 64, base + 96, st), "qlora_rope")
+    return qo, ko
+
+
+def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
+             positions: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+             interleaved: bool = False, scale: float = 1.0, out: Optional[tuple] = None,
+             stream=None):
+    """q and k (or q alone, k None) with their rotary positions: (q', k').
+
+    Dense q [B, S, H, D] and k [B, S, Hkv, D], or packed [T, H, D] and
+    [T, Hkv, D]; bf16, views as attention_fwd takes them, D a multiple of 8 up
+    to 1024.  inv_freq (float64, n elements: see rope_frequencies) turns the
+    first 2 n elements of each head, in pairs (j, n + j) or, `interleaved`,
+    (2 j, 2 j + 1); the others are copied.  scale multiplies the turned ones.
+
+    positions: int32 or int64, [B, S] (or [S] for all), packed [T]; None: a
+    row's place in its sequence, which for packed rows `cu_seqlens` gives (as in
+    attention_fwd; without it the rows are one sequence).  Rows past the last
+    offset are copied.  out: the two tensors to write, of rows that lie apart;
+    (q, k) themselves rotate in place."""
+    return _rope_call(("q", "k"), q, k, inv_freq, positions, cu_seqlens, interleaved, scale, out, 0,
+                      stream)
+
+
+def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], inv_freq: torch.Tensor,
+             positions: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+             interleaved: bool = False, scale: float = 1.0, out: Optional[tuple] = None,
+             stream=None):
+    """The gradients of rope_fwd's q and k from those of its outputs: the
+    rotation by the negative angles.  Arguments as there."""
+    return _rope_call(("dq", "dk"), dq, dk, inv_freq, positions, cu_seqlens, interleaved, scale, out,
+                      1, stream)
+
+
+class _RopeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, positions, cu_seqlens, interleaved, scale):
+        ctx.save_for_backward(inv_freq, positions, cu_seqlens)
+        ctx.how = interleaved, scale
+        ctx.set_materialize_grads(False)
+        return rope_fwd(q, k, inv_freq, positions, cu_seqlens, interleaved, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        inv_freq, positions, cu_seqlens = ctx.saved_tensors
+        how = (inv_freq, positions, cu_seqlens, *ctx.how)
+        dq, dk = (None if t is None or not need else _takeable(t)
+                  for t, need in zip((dq, dk), ctx.needs_input_grad))
+        if dq is None:   # the one that is there takes q's place
+            dk = None if dk is None else rope_bwd(dk, None, *how)[0]
+        else:
+            dq, dk = rope_bwd(dq, dk, *how)
+        return dq, dk, None, None, None, None, None
+
+
+def rope(q, k, inv_freq, positions=None, cu_seqlens=None, interleaved: bool = False,
+         scale: float = 1.0):
+    """rope_fwd with gradients for q and k (torch autograd)."""
+    return _RopeFunction.apply(q, k, inv_freq, positions, cu_seqlens, interleaved, scale)
 
 
 # ---------------------------------------------------------------------------
