@@ -354,6 +354,11 @@ def run(state):
             return {"q": q, "k": k}
         if op == "adamw":
             st = qn.AdamWState(s["m"], s["v"], s["m_scale"], s["v_scale"])
+            if s["copy"] is not None and "ends" not in s:
+                # the program's own padding between the copies, which the step does not write, cleared before the first one
+                s["ends"] = [t[t.numel() - n:] for t, n in zip(s["copy"].split([x.numel() + n for x, n in zip(s["grads"], s["pads"])]),
+                                                               s["pads"]) if n]
+                torch._foreach_zero_(s["ends"])
             qn.adamw_step(s["params"], s["grads"], st, case["step"], s["lr"], betas=s["betas"], eps=s["eps"],
                           weight_decay=s["decay"], norm=None if s["max_norm"] is None else s["norm"], max_norm=s["max_norm"],
                           copies=s["copies"])
