@@ -336,6 +336,30 @@ int32_t qlora_linear_fwd_noalloc(const nf4_tensor_t* w, const uint16_t* X,
                                  uint16_t* Y, uint16_t* U_out,
                                  hipStream_t stream);
 
+/* qlora_linear_multi_fwd -- the layer for rows of many adapters over one
+ * frozen weight (the base never changes and is shared; the adapters are small:
+ * blog section "Where the memory goes"):
+ *   Y_i = X_i W^T + s_a (X_i A_a^T) B_a^T,   a = index[i]
+ * and Y_i = X_i W^T where index[i] lies outside 0 .. n_adapters - 1.
+ *   w, X, M, Y   as in qlora_linear_fwd, M at most 2^26
+ *   A, B         [n_adapters, r, K] and [n_adapters, N, r] bf16, contiguous
+ *                (adapters of smaller rank padded with zeros), n_adapters >= 1,
+ *                1 <= r <= 256; any size together
+ *   s            [n_adapters] fp32 (device)
+ *   index        [M] int32 (device), in any order; rows of one adapter next to
+ *                each other (prompts) cost least.  Read by the kernels; any
+ *                value is allowed.
+ *   ws           >= qlora_multi_workspace_size(M, N, K, r) bytes
+ * M <= 16 streams the packed weight once, as qlora_linear_fwd does; larger M
+ * takes the MFMA tile path.  A row's result does not depend on adapters that
+ * it does not have, whatever they hold; an infinity or NaN in B gives its
+ * adapter's rows an infinity or NaN in that column. */
+size_t qlora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r);
+int32_t qlora_linear_multi_fwd(const nf4_tensor_t* w, const uint16_t* X, int64_t M,
+                               const uint16_t* A, const uint16_t* B, const float* s,
+                               int32_t n_adapters, int32_t r, const int32_t* index, uint16_t* Y,
+                               void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Measurement helper (not part of the layer): a read-only stream over
  * `bytes` bytes of device memory at src (16-byte aligned, bytes a multiple
  * of 16), the HBM read ceiling the few-token forward's weight stream is

@@ -55,6 +55,8 @@ EXPORTS = (
     "qlora_linear_fwd_ev",
     "qlora_linear_bwd_ev",
     "qlora_linear_fwd_noalloc",
+    "qlora_multi_workspace_size",
+    "qlora_linear_multi_fwd",
     "qlora_stream_read",
     "qlora_lq_workspace_size",
     "qlora_lq_init",
@@ -226,6 +228,11 @@ def lib() -> ctypes.CDLL:
     L.qlora_linear_fwd_noalloc.restype = i32
     L.qlora_linear_fwd_noalloc.argtypes = [ctypes.POINTER(Nf4Tensor), vp, i64, vp, vp, i32, f32,
                                            vp, vp, vp]
+    L.qlora_multi_workspace_size.restype = sz
+    L.qlora_multi_workspace_size.argtypes = [i64, i64, i64, i32]
+    L.qlora_linear_multi_fwd.restype = i32
+    L.qlora_linear_multi_fwd.argtypes = [ctypes.POINTER(Nf4Tensor), vp, i64, vp, vp, vp, i32, i32,
+                                         vp, vp, vp, sz, vp]
     L.qlora_stream_read.restype = i32
     L.qlora_stream_read.argtypes = [vp, sz, vp, vp]
     L.qlora_lq_workspace_size.restype = sz

@@ -40,6 +40,9 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int32_t r) {
          K <= QLORA_LINEAR_MAX_NK;
 }
 
+// Rows of qlora_linear_multi_fwd: its workgroups are counted in 24 bits.
+constexpr int64_t kMultiMaxRows = (int64_t)1 << 26;
+
 FwdPlan plan_fwd(int64_t M, int64_t N, int64_t K, int32_t r) {
   FwdPlan p{};
   const int64_t rp = rank_pad(r);
@@ -470,6 +473,36 @@ extern "C" int32_t qlora_linear_fwd_noalloc(const nf4_tensor_t* w, const uint16_
   return linear_fwd(w, X, M, A, B, r, s, Y, U_out, ws, QLORA_NOALLOC_SCRATCH_BYTES, stream,
                     nullptr, nullptr);
 }
+
+extern "C" {
+
+size_t qlora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r) {
+  if (!sizes_ok(M, N, K, r) || M > kMultiMaxRows) return 0;
+  return align_up(gemv_fits(M, r, K) ? gemv_workspace_bytes(M, r, K) : multi_down_bytes(M, K, r));
+}
+
+int32_t qlora_linear_multi_fwd(const nf4_tensor_t* w, const uint16_t* X, int64_t M,
+                               const uint16_t* A, const uint16_t* B, const float* s,
+                               int32_t n_adapters, int32_t r, const int32_t* index, uint16_t* Y,
+                               void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int32_t chk = check_fwd(w, X, M, A, B, r, 1.0f, Y, nullptr);
+  if (chk != QLORA_OK) return chk;
+  if (M > kMultiMaxRows || n_adapters < 1 || !s || ((uintptr_t)s & 3u) != 0 || !index ||
+      ((uintptr_t)index & 3u) != 0 || !ws || !aligned16(ws))
+    return QLORA_ERR_INVALID;
+  if (ws_bytes < qlora_multi_workspace_size(M, w->N, w->K, r)) return QLORA_ERR_WORKSPACE;
+  const Nf4View v = view_of(w);
+  float* part = static_cast<float*>(ws);
+  if (gemv_fits(M, r, w->K))
+    return launch_status(
+        launch_qgemv_multi(v, X, M, A, B, r, s, n_adapters, index, Y, part, stream));
+  const hipError_t e = launch_multi_down(X, M, w->K, A, r, n_adapters, index, part, stream);
+  if (e != hipSuccess) return QLORA_ERR_LAUNCH;
+  return launch_status(launch_qgemm_multi_fwd(v, X, M, part, multi_down_slices(M, w->K), B, r, s,
+                                              n_adapters, index, Y, stream));
+}
+
+}  // extern "C"
 
 extern "C" int32_t qlora_stream_read(const void* src, size_t bytes, uint32_t* sink,
                                      hipStream_t stream) {

@@ -32,6 +32,8 @@
 // block, so each MFMA contracts codes of a single block.  Word j of lane
 // group q then holds codes 32 (q & 1) + 16 (q >> 1) + 8 (j & 1) .. +7 of
 // block kb + (j >> 1); the X fragment of MFMA j uses the same positions.
+#include <type_traits>
+
 #include "kernels.hpp"
 
 namespace qn {
@@ -62,10 +64,42 @@ constexpr int kPastEnd = INT32_MIN;
 // Grid (S, ceil(r / 64)); wave w of a workgroup owns adapter rows
 // 64 blockIdx.y + 16 w .. +15.  MFMA 16x16x32: A = X rows, B = A rows.
 // ---------------------------------------------------------------------------
+// Rows of many adapters (kMulti): grid dimension z over the rows; the first
+// row of an adapter brings it in, for all its rows, and a row without one
+// gets zeros.
+// ---------------------------------------------------------------------------
+struct Owners {
+  const int32_t* index;  // [M]: adapter of each row
+  int adapters;          // index outside 0 .. adapters - 1: none
+};
+__device__ __forceinline__ int owner_of(const Owners& o, int64_t row) {
+  const int a = o.index[row];
+  return (unsigned)a < (unsigned)o.adapters ? a : -1;
+}
+
+template <bool kMulti>
 __global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restrict__ X, int64_t M,
                                                         const uint16_t* __restrict__ A, int32_t r,
                                                         int64_t K, int64_t slice,
-                                                        float* __restrict__ part) {
+                                                        float* __restrict__ part, Owners own) {
+  uint32_t rows = 0xffffu;  // the rows that this workgroup computes
+  if constexpr (kMulti) {
+    const int z = blockIdx.z;
+    const int al = threadIdx.x % 64 < M ? owner_of(own, threadIdx.x % 64) : -2;
+    const int a = __builtin_amdgcn_readlane(al, z);
+    rows = (uint32_t)__builtin_amdgcn_ballot_w64(al == a);
+    if (a < 0) {
+      // zeros for this row alone
+      if (threadIdx.x < 64 && blockIdx.x == 0)
+        for (int64_t e = threadIdx.x; e < 64 * kGemvMaxSlices; e += 64) {
+          const int64_t j = (int64_t)blockIdx.y * 64 + e / kGemvMaxSlices;
+          if (j < r) part[(z * (int64_t)r + j) * kGemvMaxSlices + e % kGemvMaxSlices] = 0.0f;
+        }
+      return;
+    }
+    if (rows & ((1u << z) - 1)) return;  // an earlier row's workgroup does it
+    A += (int64_t)a * r * K;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i16 = lane & 15, q = lane >> 4;
   const int64_t j = (int64_t)blockIdx.y * 64 + wave * 16 + i16;
@@ -102,7 +136,8 @@ __global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restri
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int m = 4 * q + v;
-    if (m < M && jvalid) part[(m * r + j) * kGemvMaxSlices + blockIdx.x] = acc[v];
+    if (m < M && jvalid && (rows >> m & 1))
+      part[(m * r + j) * kGemvMaxSlices + blockIdx.x] = acc[v];
   }
   // the slices past the grid read as zeros, so that a sum may take all of
   // them in order
@@ -110,7 +145,7 @@ __global__ __launch_bounds__(256) void k_lora_down_part(const uint16_t* __restri
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int m = 4 * q + v;
-      if (m < M && jvalid)
+      if (m < M && jvalid && (rows >> m & 1))
         for (int s = gridDim.x; s < kGemvMaxSlices; ++s)
           part[(m * r + j) * kGemvMaxSlices + s] = 0.0f;
     }
@@ -131,6 +166,11 @@ struct GemvArgs {
   uint16_t* U_out;  // nullable, bf16 [M][r]
   int bshift;       // block size 64 << bshift
   UserTable ut;     // the caller's codebook (CodeUser types only)
+};
+// Rows of many adapters: B is that of all, s and U_out are not used.
+struct MultiGemvArgs : GemvArgs {
+  Owners own;
+  const float* scales;  // [adapters]
 };
 
 #ifndef QN_GEMV_PD
@@ -156,10 +196,11 @@ __host__ __device__ constexpr int64_t gemv_lds_words(int G, int KW, int64_t M, i
 
 // One row group runs two workgroups per CU (16 waves): the register budget
 // is held to 128 so that both fit.
-template <int G, int KW, int PD, class CT>
+template <int G, int KW, int PD, class CT, class Args>
 __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(G == 1 ? 4 : 1)))
-void k_qgemv(GemvArgs p) {
+void k_qgemv(Args p) {
   constexpr int NT = 64 * KW;
+  constexpr bool kMulti = std::is_same_v<Args, MultiGemvArgs>;
   extern __shared__ float lds[];
   uint32_t* lut = reinterpret_cast<uint32_t*>(lds);
   float* ush = lds + kLutWords;
@@ -358,7 +399,7 @@ void k_qgemv(GemvArgs p) {
   // loads go through buffer resources (an offset past the end reads 0), so
   // none sits behind a branch, and all of them are issued before the first
   // use: the prologue costs about one memory latency.
-  const bool b_lds = kRowMajor && (p.r & 7) == 0;  // uniform
+  const bool b_lds = kRowMajor && !kMulti && (p.r & 7) == 0;  // uniform
   if (b_lds) {
     // direct-to-LDS copy of rows n0 .. n0 + 16 G - 1 of B (1 KB per wave
     // instruction; bytes past B read 0), waited for before the epilogue
@@ -623,6 +664,57 @@ void k_qgemv(GemvArgs p) {
     yk[k] = y;
     lk[k] = 0.0f;
   }
+  if constexpr (kMulti) {
+    // Every output has the adapter rows of its token.  Tokens without an
+    // adapter, and outputs that are not stored, read the first rows and drop
+    // what comes of it.
+    const uint16_t* bp[KO];
+    float sk[KO];
+    bool has[KO];
+#pragma unroll
+    for (int k = 0; k < KO; ++k) {
+      const int a = vk[k] ? owner_of(p.own, mk[k]) : -1;
+      has[k] = a >= 0;
+      sk[k] = has[k] ? p.scales[a] : 0.0f;
+      bp[k] = p.B + (has[k] ? ((int64_t)a * N + nk[k]) * p.r : 0);
+    }
+    float sum[KO];
+#pragma unroll
+    for (int k = 0; k < KO; ++k) sum[k] = 0.0f;
+    if ((p.r & 7) == 0) {
+      for (int j0 = 0; j0 < p.r; j0 += JB) {
+        u32x4 bq[KO][JB / 8];
+#pragma unroll
+        for (int k = 0; k < KO; ++k)
+#pragma unroll
+          for (int q = 0; q < JB / 8; ++q)
+            bq[k][q] = *reinterpret_cast<const u32x4*>(bp[k] + (j0 + 8 * q < p.r ? j0 + 8 * q : 0));
+        __builtin_amdgcn_sched_barrier(0);  // every load of the batch before the first use
+#pragma unroll
+        for (int q = 0; q < JB / 8; ++q) {
+          if (j0 + 8 * q >= p.r) break;  // uniform
+#pragma unroll
+          for (int k = 0; k < KO; ++k) {
+            const float* ur8 = ush + (has[k] ? mk[k] * p.r : 0) + j0 + 8 * q;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              const uint32_t wd = bq[k][q][t >> 1];
+              sum[k] += ur8[t] * ((t & 1) ? bf16_hi_to_f32(wd) : bf16_lo_to_f32(wd));
+            }
+          }
+        }
+      }
+    } else {
+      for (int j = 0; j < p.r; ++j)
+#pragma unroll
+        for (int k = 0; k < KO; ++k) sum[k] += ush[(has[k] ? mk[k] * p.r : 0) + j] * bf16_to_f32(bp[k][j]);
+    }
+#pragma unroll
+    for (int k = 0; k < KO; ++k)
+      if (vk[k])
+        p.Y[mk[k] * N + nk[k]] = f32_to_bf16(has[k] ? yk[k] + sk[k] * sum[k] : yk[k]);
+    return;
+  }
   if ((p.r & 7) == 0) {
     // r a multiple of 8: 16-byte adapter reads (8 columns, from LDS with
     // seven groups) and 16-byte U reads; JB columns per batch.  Outputs
@@ -688,10 +780,7 @@ void k_qgemv(GemvArgs p) {
 
 }  // namespace
 
-bool gemv_fits(int64_t M, int32_t r, int64_t K) {
-  // the workgroup's LDS within 96 KB (K up to about 32000 at 16 tokens and rank 256)
-  return M <= kGemvMaxM && 4 * gemv_lds_words(2, 8, M, r, K / 64) <= 96 * 1024;
-}
+namespace {
 
 int gemv_lora_slices(int64_t M, int32_t r, int64_t K) {
   static_assert(kGemvMaxSlices == 32, "at most 32 slices below");
@@ -705,43 +794,29 @@ int gemv_lora_slices(int64_t M, int32_t r, int64_t K) {
   return (int)s;
 }
 
-size_t gemv_workspace_bytes(int64_t M, int32_t r, int64_t K) {
-  (void)K;
-  return (size_t)kGemvMaxSlices * M * r * sizeof(float);
-}
-
-template <int G>
-hipError_t launch_qgemv_g(const GemvArgs& a, int code, hipStream_t stream) {
+template <int G, class Args>
+hipError_t launch_qgemv_g(const Args& a, int code, hipStream_t stream) {
   // seven row groups run the row-group-major loop; their ring of steps only
   // serves an odd tail block, one slot in flight
   constexpr int KW = 8, PD = G == 7 ? 2 : QN_GEMV_PD;
   const size_t lds = 4 * (size_t)gemv_lds_words(G, KW, a.M, a.r, a.K / 64);
   const dim3 grid((unsigned)((a.N + 16 * G - 1) / (16 * G)));
   return with_any_code(code, [&](auto ct) {
-    const void* fn = reinterpret_cast<const void*>(&k_qgemv<G, KW, PD, decltype(ct)>);
+    const void* fn = reinterpret_cast<const void*>(&k_qgemv<G, KW, PD, decltype(ct), Args>);
     // dynamic LDS above the default 64 KB needs the limit raised; the call is
     // cheap and idempotent, and made for the device the launch goes to
     // (a per-process cache would only cover the first device)
     hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (G == 7 ? 160 : 96) * 1024);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_qgemv<G, KW, PD, decltype(ct)>), grid, dim3(64 * KW), lds, stream, a);
+    hipLaunchKernelGGL((k_qgemv<G, KW, PD, decltype(ct), Args>), grid, dim3(64 * KW), lds, stream, a);
     return hipGetLastError();
   });
 }
 
-hipError_t launch_qgemv(const Nf4View& w, const uint16_t* X, int64_t M, const uint16_t* A,
-                        const uint16_t* B, int32_t r, float s, uint16_t* Y, uint16_t* U_out,
-                        float* upart, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1) {
-  const int us = gemv_lora_slices(M, r, w.K);
-  const int64_t slice = (w.K / us + 31) / 32 * 32;
-  dim3 gu((unsigned)((w.K + slice - 1) / slice), (unsigned)((r + 63) / 64));
-  hipLaunchKernelGGL(k_lora_down_part, gu, dim3(256), 0, stream, X, M, A, r, w.K, slice, upart);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (ev0 && (e = hipEventRecord(ev0, stream)) != hipSuccess) return e;
-  const GemvArgs a{w.codes, w.q8, w.step, X,     M, w.N, w.K,  upart,
-                   B,       r,    s,      Y, U_out, w.bshift, w.ut};
+// The weight stream with the row groups that fit the chip.
+template <class Args>
+hipError_t launch_stream(const Args& a, const Nf4View& w, hipStream_t stream) {
   const int64_t kblocks = w.K / 64;
   // 16 G weight rows per workgroup, K split over its 8 waves.
   //  - G = 7 when the 16-row groups make exactly one workgroup of 7 per CU
@@ -760,14 +835,61 @@ hipError_t launch_qgemv(const Nf4View& w, const uint16_t* X, int64_t M, const ui
     cus = 0;
   const int64_t groups = (w.N + 15) / 16;
   const bool g7 = cus > 0 && groups % (7 * (int64_t)cus) == 0 &&
-                  4 * gemv_lds_words(7, 8, M, r, kblocks) <= 160 * 1024;
-  const bool g1 = !g7 && M <= 2 && cus > 0 && groups < 2 * (int64_t)cus;
-  e = g7   ? launch_qgemv_g<7>(a, w.code, stream)
-      : g1 ? launch_qgemv_g<1>(a, w.code, stream)
-           : launch_qgemv_g<2>(a, w.code, stream);
+                  4 * gemv_lds_words(7, 8, a.M, a.r, kblocks) <= 160 * 1024;
+  const bool g1 = !g7 && a.M <= 2 && cus > 0 && groups < 2 * (int64_t)cus;
+  return g7   ? launch_qgemv_g<7>(a, w.code, stream)
+         : g1 ? launch_qgemv_g<1>(a, w.code, stream)
+              : launch_qgemv_g<2>(a, w.code, stream);
+}
+
+}  // namespace
+
+// qgemv_multi.hip compiles this file a second time for the many-adapter
+// forward, so that the two halves of the kernels build at the same time.
+#ifdef QN_GEMV_MULTI
+hipError_t launch_qgemv_multi(const Nf4View& w, const uint16_t* X, int64_t M, const uint16_t* A,
+                              const uint16_t* B, int32_t r, const float* scales, int adapters,
+                              const int32_t* index, uint16_t* Y, float* upart, hipStream_t stream) {
+  const int us = gemv_lora_slices(M, r, w.K);
+  const int64_t slice = (w.K / us + 31) / 32 * 32;
+  const Owners own{index, adapters};
+  const dim3 gu((unsigned)((w.K + slice - 1) / slice), (unsigned)((r + 63) / 64), (unsigned)M);
+  k_lora_down_part<true><<<gu, dim3(256), 0, stream>>>(X, M, A, r, w.K, slice, upart, own);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const MultiGemvArgs a{{w.codes, w.q8, w.step, X, M, w.N, w.K, upart, B, r, 0.0f, Y, nullptr,
+                         w.bshift, w.ut}, own, scales};
+  return launch_stream(a, w, stream);
+}
+#else
+bool gemv_fits(int64_t M, int32_t r, int64_t K) {
+  // the workgroup's LDS within 96 KB (K up to about 32000 at 16 tokens and rank 256)
+  return M <= kGemvMaxM && 4 * gemv_lds_words(2, 8, M, r, K / 64) <= 96 * 1024;
+}
+
+size_t gemv_workspace_bytes(int64_t M, int32_t r, int64_t K) {
+  (void)K;
+  return (size_t)kGemvMaxSlices * M * r * sizeof(float);
+}
+
+hipError_t launch_qgemv(const Nf4View& w, const uint16_t* X, int64_t M, const uint16_t* A,
+                        const uint16_t* B, int32_t r, float s, uint16_t* Y, uint16_t* U_out,
+                        float* upart, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1) {
+  const int us = gemv_lora_slices(M, r, w.K);
+  const int64_t slice = (w.K / us + 31) / 32 * 32;
+  dim3 gu((unsigned)((w.K + slice - 1) / slice), (unsigned)((r + 63) / 64));
+  hipLaunchKernelGGL(k_lora_down_part<false>, gu, dim3(256), 0, stream, X, M, A, r, w.K, slice, upart,
+                     Owners{});
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (ev0 && (e = hipEventRecord(ev0, stream)) != hipSuccess) return e;
+  const GemvArgs a{w.codes, w.q8, w.step, X,     M, w.N, w.K,  upart,
+                   B,       r,    s,      Y, U_out, w.bshift, w.ut};
+  e = launch_stream(a, w, stream);
   if (e != hipSuccess) return e;
   if (ev1) e = hipEventRecord(ev1, stream);
   return e;
 }
+#endif
 
 }  // namespace qn

@@ -53,6 +53,25 @@ hipError_t launch_qgemv(const Nf4View& w, const uint16_t* X, int64_t M, const ui
                         const uint16_t* B, int32_t r, float s, uint16_t* Y, uint16_t* U_out,
                         float* upart, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
 
+// ---- rows of many adapters (qgemm_multi.hip, qgemv_multi.hip, multi.hip) ----
+// Row i has the adapter index[i] (device; none outside 0 .. adapters - 1); A
+// [adapters, r, K], B [adapters, N, r], scales [adapters] fp32.
+// M <= kGemvMaxM (workspace as launch_qgemv's):
+hipError_t launch_qgemv_multi(const Nf4View& w, const uint16_t* X, int64_t M, const uint16_t* A,
+                              const uint16_t* B, int32_t r, const float* scales, int adapters,
+                              const int32_t* index, uint16_t* Y, float* upart, hipStream_t stream);
+// Other M: part[s][m][j] = the sum over K slice s of X[m] A_index[m][j], zeros
+// for r <= j < ceil(r / 8) * 8, nothing for rows without an adapter ...
+int multi_down_slices(int64_t M, int64_t K);
+size_t multi_down_bytes(int64_t M, int64_t K, int32_t r);
+hipError_t launch_multi_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A, int32_t r,
+                             int adapters, const int32_t* index, float* part, hipStream_t stream);
+// ... which the tile kernels take.
+hipError_t launch_qgemm_multi_fwd(const Nf4View& w, const uint16_t* X, int64_t M,
+                                  const float* part, int slices, const uint16_t* B, int32_t r,
+                                  const float* scales, int adapters, const int32_t* index,
+                                  uint16_t* Y, hipStream_t stream);
+
 // ---- lora.hip: small-rank products with in-kernel reduction of contraction slices ----
 // Operand element access: A-op (i, c) at a[i*a_si + c*a_sc]; B-op (c, j) at
 // b[j*b_sj + c*b_sc]; one stride of each operand must be 1.

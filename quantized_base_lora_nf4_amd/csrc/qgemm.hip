@@ -400,14 +400,157 @@ struct FwdArgs {
   UserTable ut;  // the caller's codebook (CodeUser types only)
 };
 
+// Rows of many adapters: row i has the adapter index[i] (none outside 0 ..
+// adapters - 1).  U arrives as fp32 partial sums of X A^T (multi.hip), B and
+// the scales are those of all adapters; U, ldu and s above are not used.
+struct MultiFwdArgs : FwdArgs {
+  const float* part;     // [slices][M][ceil(r / 8) * 8], zero-padded
+  int slices;
+  const float* scales;   // [adapters]
+  const int32_t* index;  // [M]
+  int adapters;
+};
+
+// The tile's LoRA term with many adapters, as more contraction steps on the
+// same accumulators: the ranks of the adapters that the tile's rows have, one
+// after the other in units of 8, make the contraction, and a row's operand is
+// bf16(s U) in its own adapter's units and zero in the others.  One 64-deep
+// step takes 8 units, so that 8 adapters of rank 8 cost what one of rank 64
+// does, and rows need no order (256 rows of 64 adapters of rank 16: 16 steps
+// beside the 64 of K = 4096; in runs of rows, one or two).
+// Zero times an infinity or NaN of another row's adapter would not be zero:
+// such elements of B are staged as zeros and noted, by adapter and column,
+// and the adapter's own rows get NaN in those columns at the end.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+template <class C>
+__device__ __forceinline__ void multi_lora(const MultiFwdArgs& p, uint16_t* As, uint16_t* Bs,
+                                           int64_t m0, int64_t n0, int wm, int wn, int lane, int tid,
+                                           AccT<C>& acc) {
+  constexpr int kWaves = C::BM / 64;  // waves that look at the tile's rows
+  constexpr int kWords = C::BN / 32;
+  __shared__ __attribute__((aligned(16))) int owner[C::BM];  // adapter, then its place in `list`
+  __shared__ int list[C::BM], place[C::BM];
+  __shared__ int found[kWaves];
+  __shared__ uint32_t odd[C::BM * kWords];  // columns with an infinity or NaN, by place
+  __shared__ int any_odd;
+  int a = -1, lead = tid;
+  if (tid < C::BM) {
+    if (m0 + tid < p.M) a = p.index[m0 + tid];
+    if ((unsigned)a >= (unsigned)p.adapters) a = -1;
+    owner[tid] = a;
+  }
+  for (int e = tid; e < C::BM * kWords; e += C::NT) odd[e] = 0;
+  if (tid == 0) any_odd = 0;
+  __syncthreads();
+  // the adapters of the tile in the order of their first rows (`lead`)
+  uint64_t mask = 0;
+  if (tid < C::BM) {
+    const int end = (tid | 63) + 1;  // the wave's last row: the same trips in every lane
+    for (int t = 0; t < end; t += 4) {
+      const i32x4 v = *reinterpret_cast<const i32x4*>(owner + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (v[i] == a && t + i < lead) lead = t + i;
+    }
+    mask = __builtin_amdgcn_ballot_w64(a >= 0 && lead == tid);
+    if (lane == 0) found[tid >> 6] = __builtin_popcountll(mask);
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (tid >> 6 == w && (mask >> lane & 1)) {
+      const int at = count + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
+      list[at] = a;
+      place[tid] = at;
+    }
+    count += found[w];
+  }
+  __syncthreads();
+  if (tid < C::BM) owner[tid] = a >= 0 ? place[lead] : -1;
+  __syncthreads();
+  const int units = (p.r + 7) >> 3, total = count * units;  // units of an adapter, of the tile
+  const int64_t ldp = 8 * units;
+  const bool bvec = (p.r & 7) == 0;
+  for (int q0 = 0; q0 < total; q0 += 8) {
+    for (int e = tid; e < C::BM * 8; e += C::NT) {
+      const int row = e >> 3, c8 = e & 7, q = q0 + c8;
+      const int ai = q / units;
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (q < total && owner[row] == ai) {
+        const float* src = p.part + (m0 + row) * ldp + 8 * (q - ai * units);
+        f32x4 x = *reinterpret_cast<const f32x4*>(src), y = *reinterpret_cast<const f32x4*>(src + 4);
+        for (int s = 1; s < p.slices; ++s) {  // in order
+          src += p.M * ldp;
+          x += *reinterpret_cast<const f32x4*>(src);
+          y += *reinterpret_cast<const f32x4*>(src + 4);
+        }
+        const float sc = p.scales[list[ai]];
+        v = u32x4{pack_bf16x2(x[0] * sc, x[1] * sc), pack_bf16x2(x[2] * sc, x[3] * sc),
+                  pack_bf16x2(y[0] * sc, y[1] * sc), pack_bf16x2(y[2] * sc, y[3] * sc)};
+      }
+      *reinterpret_cast<u32x4*>(As + a_off(row, c8)) = v;
+    }
+    for (int e = tid; e < C::BN * 8; e += C::NT) {
+      const int row = e >> 3, c8 = e & 7, q = q0 + c8;
+      int64_t g = n0 + row;
+      if (g >= p.N) g = p.N - 1;
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (q < total) {
+        const int ai = q / units, j = 8 * (q - ai * units);
+        const uint16_t* src = p.B + ((int64_t)list[ai] * p.N + g) * p.r + j;
+        if (bvec) {
+          v = *reinterpret_cast<const u32x4*>(src);
+        } else {
+          uint16_t t[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = j + i < p.r ? src[i] : (uint16_t)0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = (uint32_t)t[2 * i] | ((uint32_t)t[2 * i + 1] << 16);
+        }
+        // bit 15 of a half: its exponent is all ones
+        u32x4 top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        if (top[0] | top[1] | top[2] | top[3]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] &= ~((top[i] >> 15) * 0xffffu);
+          atomicOr(&odd[ai * kWords + (row >> 5)], 1u << (row & 31));
+          any_odd = 1;
+        }
+      }
+      *reinterpret_cast<u32x4*>(Bs + row * LDA + c8 * 8) = v;
+    }
+    __syncthreads();
+    mma_step<C, false>(As, Bs, wm, wn, lane, acc);
+    __syncthreads();
+  }
+  if (any_odd) {  // uniform
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const int col = wn * C::FN * 32 + j * 32 + (lane & 31);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int at = owner[wm * C::FM * 32 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
+          if (at >= 0 && (odd[at * kWords + (col >> 5)] >> (col & 31) & 1))
+            acc.v[i][j][v] = __builtin_nanf("");
+        }
+      }
+  }
+}
+
 // kQ4: K is a multiple of 256 (and q8 16-byte aligned, as the C ABI
 // requires), so the constants of four consecutive blocks of a weight row are
 // one aligned 32-bit word (and share one second-level step: 4 divides 256).  The row's constants are then
 // loaded once per four steps instead of a byte and a float per step.
 // BS: block size 64 << BS (one 8-bit constant per 64 << BS weights of a row;
 // kQ4 only with BS = 0).
-template <class C, class CT, bool kQ4, int BS>
-__global__ __launch_bounds__(C::NT, 1) void k_qgemm_fwd(FwdArgs p) {
+// Args: FwdArgs, or MultiFwdArgs for rows of many adapters.
+template <class C, class CT, bool kQ4, int BS, class Args>
+__global__ __launch_bounds__(C::NT, 1) void k_qgemm_fwd(Args p) {
   static_assert(!kQ4 || BS == 0, "grouped constants need 64-element blocks");
   // One LDS object per buffer: the compiler's wait for a direct-to-LDS load
   // then applies only to reads of the buffer that load writes.
@@ -563,6 +706,11 @@ __global__ __launch_bounds__(C::NT, 1) void k_qgemm_fwd(FwdArgs p) {
   else
     run(std::false_type{});
 
+  if constexpr (std::is_same_v<Args, MultiFwdArgs>) {
+    multi_lora<C>(p, xs0, ws0, m0, n0, wm, wn, lane, tid, acc);
+    store_tile<C>(p.Y, N, m0, n0, M, N, wm, wn, lane, acc);
+    return;
+  }
   // LoRA: extra contraction over r with A-side bf16(s U) and B-side B.
   const bool bvec = (p.r & 7) == 0;
   for (int j0 = 0; j0 < p.r; j0 += 64) {
@@ -776,27 +924,27 @@ bool small_tiles(int64_t M, int64_t cols) {
   return 2 * big <= device_cus();
 }
 
-template <class C>
-hipError_t launch_fwd(const FwdArgs& a, const Nf4View& w, int64_t M, hipStream_t stream) {
+template <class C, class Args>
+hipError_t launch_fwd(const Args& a, const Nf4View& w, int64_t M, hipStream_t stream) {
   dim3 grid((unsigned)(((w.N + C::BN - 1) / C::BN) * ((M + C::BM - 1) / C::BM)));
   const bool q4 = (w.K % 256) == 0 && w.bshift == 0;
   with_any_code(w.code, [&](auto ct) {
     using CT = decltype(ct);
     if (q4)
-      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, true, 0>), grid, dim3(C::NT), 0, stream, a);
+      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, true, 0, Args>), grid, dim3(C::NT), 0, stream, a);
     else if (w.bshift == 2)
-      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, false, 2>), grid, dim3(C::NT), 0, stream, a);
+      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, false, 2, Args>), grid, dim3(C::NT), 0, stream, a);
     else if (w.bshift == 1)
-      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, false, 1>), grid, dim3(C::NT), 0, stream, a);
+      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, false, 1, Args>), grid, dim3(C::NT), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, false, 0>), grid, dim3(C::NT), 0, stream, a);
+      hipLaunchKernelGGL((k_qgemm_fwd<C, CT, false, 0, Args>), grid, dim3(C::NT), 0, stream, a);
     return 0;
   });
   return hipGetLastError();
 }
 
 template <class C>
-hipError_t launch_bwd(const BwdArgs& a, const Nf4View& w, int64_t M, hipStream_t stream) {
+[[maybe_unused]] hipError_t launch_bwd(const BwdArgs& a, const Nf4View& w, int64_t M, hipStream_t stream) {
   dim3 grid((unsigned)(((w.K + C::BN - 1) / C::BN) * ((M + C::BM - 1) / C::BM)));
   with_any_code(w.code, [&](auto ct) {
     using CT = decltype(ct);
@@ -813,6 +961,19 @@ hipError_t launch_bwd(const BwdArgs& a, const Nf4View& w, int64_t M, hipStream_t
 
 }  // namespace
 
+// qgemm_multi.hip compiles this file a second time for the many-adapter
+// forward, so that the two halves of the kernels build at the same time.
+#ifdef QN_QGEMM_MULTI
+hipError_t launch_qgemm_multi_fwd(const Nf4View& w, const uint16_t* X, int64_t M,
+                                  const float* part, int slices, const uint16_t* B, int32_t r,
+                                  const float* scales, int adapters, const int32_t* index,
+                                  uint16_t* Y, hipStream_t stream) {
+  const MultiFwdArgs a{{X, w.codes, w.q8, w.step, nullptr, 0, B, r, 0.0f, Y, M, w.N, w.K, w.ut},
+                       part, slices, scales, index, adapters};
+  return small_tiles(M, w.N) ? launch_fwd<SmallCfg>(a, w, M, stream)
+                             : launch_fwd<GemmCfg>(a, w, M, stream);
+}
+#else
 hipError_t launch_qgemm_fwd(const Nf4View& w, const uint16_t* X, int64_t M, const uint16_t* U,
                             int64_t ldu, const uint16_t* B, int32_t r, float s, uint16_t* Y,
                             hipStream_t stream) {
@@ -828,5 +989,7 @@ hipError_t launch_qgemm_bwd(const Nf4View& w, const uint16_t* dY, int64_t M, con
   return small_tiles(M, w.K) ? launch_bwd<SmallCfg>(a, w, M, stream)
                              : launch_bwd<GemmCfg>(a, w, M, stream);
 }
+
+#endif
 
 }  // namespace qn
