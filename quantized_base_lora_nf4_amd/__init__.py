@@ -7,9 +7,11 @@ tensors into its calls (see :mod:`quantized_base_lora_nf4_amd.ops`).
 
 from ._lib import LIB_PATH, EXPORTS, QloraError, lib  # noqa: F401
 from .ops import (LqResult, NF4Weight, QLoRALinear, QLoRALinearFunction,  # noqa: F401
-                  QLoRAMultiLinear, alloc_nf4, code_table, ilp_plan, lq_init, lq_workspace_size,
-                  multi_workspace_size, nf4_dequantize, nf4_quantize, qlora_linear_bwd,
-                  qlora_linear_fwd, qlora_linear_fwd_noalloc, qlora_linear_multi_fwd, quant_error, storage_bytes, user_table, workspace_size, USER_CODES)
+                  alloc_nf4, code_table, ilp_plan, lq_init, lq_workspace_size, nf4_dequantize,
+                  nf4_quantize, qlora_linear_bwd, qlora_linear_fwd, qlora_linear_fwd_noalloc,
+                  quant_error, storage_bytes, user_table, workspace_size, USER_CODES)
+from .multi_ops import (QLoRAMultiLinear, multi_workspace_size,  # noqa: F401
+                        qlora_linear_multi_fwd)
 from .optim import AdamW, AdamWState, adamw_init, adamw_step, adamw_values  # noqa: F401
 from .train_ops import (LayerNorm, RMSNorm, attention, attention_bwd, attention_fwd,  # noqa: F401
                         clip_grad_norm, grad_norm, norm, norm_bwd, norm_fwd, rope, rope_bwd,

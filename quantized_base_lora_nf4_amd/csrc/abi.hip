@@ -478,7 +478,9 @@ extern "C" {
 
 size_t qlora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r) {
   if (!sizes_ok(M, N, K, r) || M > kMultiMaxRows) return 0;
-  return align_up(gemv_fits(M, r, K) ? gemv_workspace_bytes(M, r, K) : multi_down_bytes(M, K, r));
+  if (gemv_fits(M, r, K)) return align_up(gemv_workspace_bytes(M, r, K));
+  return align_up(multi_down_bytes(M, K, r)) +
+         align_up(qrows_takes(M, N, K, r) ? multi_xfrag_bytes(M, K) : (size_t)M * 4);
 }
 
 int32_t qlora_linear_multi_fwd(const nf4_tensor_t* w, const uint16_t* X, int64_t M,
@@ -490,16 +492,33 @@ int32_t qlora_linear_multi_fwd(const nf4_tensor_t* w, const uint16_t* X, int64_t
   if (M > kMultiMaxRows || n_adapters < 1 || !s || ((uintptr_t)s & 3u) != 0 || !index ||
       ((uintptr_t)index & 3u) != 0 || !ws || !aligned16(ws))
     return QLORA_ERR_INVALID;
-  if (ws_bytes < qlora_multi_workspace_size(M, w->N, w->K, r)) return QLORA_ERR_WORKSPACE;
+  const int64_t N = w->N, K = w->K;
+  if (ws_bytes < qlora_multi_workspace_size(M, N, K, r)) return QLORA_ERR_WORKSPACE;
   const Nf4View v = view_of(w);
   float* part = static_cast<float*>(ws);
-  if (gemv_fits(M, r, w->K))
+  if (gemv_fits(M, r, K))
     return launch_status(
         launch_qgemv_multi(v, X, M, A, B, r, s, n_adapters, index, Y, part, stream));
-  const hipError_t e = launch_multi_down(X, M, w->K, A, r, n_adapters, index, part, stream);
+  const bool rows = qrows_takes(M, N, K, r);
+  // U's partial sums, then X in the other order (qrows.hip) or the rows' order
+  char* const rest = static_cast<char*>(ws) + align_up(multi_down_bytes(M, K, r));
+  uint16_t* xfrag = nullptr;
+  int32_t* order = nullptr;
+  hipError_t e;
+  if (rows) {
+    xfrag = reinterpret_cast<uint16_t*>(rest);
+  } else if (multi_order_takes(K)) {
+    order = reinterpret_cast<int32_t*>(rest);
+    e = launch_multi_order(index, M, n_adapters, order, stream);
+    if (e != hipSuccess) return QLORA_ERR_LAUNCH;
+  }
+  e = launch_multi_down(X, M, K, A, r, s, n_adapters, index, order, part, xfrag, stream);
   if (e != hipSuccess) return QLORA_ERR_LAUNCH;
-  return launch_status(launch_qgemm_multi_fwd(v, X, M, part, multi_down_slices(M, w->K), B, r, s,
-                                              n_adapters, index, Y, stream));
+  const int slices = multi_down_slices(M, K);
+  return launch_status(rows ? launch_qrows(v, xfrag, M, part, slices, B, r, n_adapters, index, Y,
+                                           stream)
+                            : launch_qgemm_multi_fwd(v, X, M, part, slices, B, r, n_adapters, index,
+                                                     order, Y, stream));
 }
 
 }  // extern "C"

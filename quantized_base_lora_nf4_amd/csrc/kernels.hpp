@@ -53,23 +53,40 @@ hipError_t launch_qgemv(const Nf4View& w, const uint16_t* X, int64_t M, const ui
                         const uint16_t* B, int32_t r, float s, uint16_t* Y, uint16_t* U_out,
                         float* upart, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
 
-// ---- rows of many adapters (qgemm_multi.hip, qgemv_multi.hip, multi.hip) ----
+// ---- rows of many adapters (qgemm_multi.hip, qgemv_multi.hip, qrows.hip, multi.hip) ----
 // Row i has the adapter index[i] (device; none outside 0 .. adapters - 1); A
 // [adapters, r, K], B [adapters, N, r], scales [adapters] fp32.
 // M <= kGemvMaxM (workspace as launch_qgemv's):
 hipError_t launch_qgemv_multi(const Nf4View& w, const uint16_t* X, int64_t M, const uint16_t* A,
                               const uint16_t* B, int32_t r, const float* scales, int adapters,
                               const int32_t* index, uint16_t* Y, float* upart, hipStream_t stream);
-// Other M: part[s][m][j] = the sum over K slice s of X[m] A_index[m][j], zeros
-// for r <= j < ceil(r / 8) * 8, nothing for rows without an adapter ...
+// Other M: for the tile kernels, the rows in an order that keeps adapters
+// together (null: as they are; always null for qrows.hip), ...
+constexpr int kMultiWindow = 4096;  // rows that are put in order together
+bool multi_order_takes(int64_t K);
+hipError_t launch_multi_order(const int32_t* index, int64_t M, int adapters, int32_t* order,
+                              hipStream_t stream);
+// ... part[s][m][j] = scale times the sum over K slice s of X A_index[j] of the
+// m-th row, zeros for r <= j < ceil(r / 8) * 8, nothing for rows without an
+// adapter, and, if xfrag is not null, X in the order of qrows.hip's MFMA
+// operands (multi_xfrag_bytes), ...
 int multi_down_slices(int64_t M, int64_t K);
 size_t multi_down_bytes(int64_t M, int64_t K, int32_t r);
+size_t multi_xfrag_bytes(int64_t M, int64_t K);
 hipError_t launch_multi_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A, int32_t r,
-                             int adapters, const int32_t* index, float* part, hipStream_t stream);
-// ... which the tile kernels take.
+                             const float* scales, int adapters, const int32_t* index,
+                             const int32_t* order, float* part, uint16_t* xfrag,
+                             hipStream_t stream);
+// ... which the kernel for batches of rows takes (qrows.hip) ...
+constexpr int kQRowsMaxM = 4096;
+bool qrows_takes(int64_t M, int64_t N, int64_t K, int32_t r);
+hipError_t launch_qrows(const Nf4View& w, const uint16_t* xfrag, int64_t M, const float* part,
+                        int slices, const uint16_t* B, int32_t r, int adapters,
+                        const int32_t* index, uint16_t* Y, hipStream_t stream);
+// ... and the tile kernels.
 hipError_t launch_qgemm_multi_fwd(const Nf4View& w, const uint16_t* X, int64_t M,
                                   const float* part, int slices, const uint16_t* B, int32_t r,
-                                  const float* scales, int adapters, const int32_t* index,
+                                  int adapters, const int32_t* index, const int32_t* order,
                                   uint16_t* Y, hipStream_t stream);
 
 // ---- lora.hip: small-rank products with in-kernel reduction of contraction slices ----

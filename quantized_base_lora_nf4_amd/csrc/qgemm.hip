@@ -187,6 +187,17 @@ __device__ __forceinline__ void load_rows_lds(uint16_t* As, __amdgpu_buffer_rsrc
   }
 }
 
+// The same with the byte offsets of this lane's rows and chunks given.
+template <class C>
+__device__ __forceinline__ void load_rows_at(uint16_t* As, __amdgpu_buffer_rsrc_t rsrc,
+                                             const int* voff, int soff, int wave) {
+#pragma unroll
+  for (int q = 0; q < C::XLD; ++q)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void*)(As + 8 * (q * (C::NT / 64) + wave) * 64), 16,
+        voff[q], soff, 0, 0);
+}
+
 __device__ __forceinline__ void wait_vmem() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // End of a pipelined step: this wave's direct-to-LDS tile loads (issued
@@ -308,6 +319,27 @@ __device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int64_t ro
     }
 }
 
+// store_tile with row i of the tile at row at[i] (LDS; -1: none).
+template <class C>
+__device__ __forceinline__ void store_at(uint16_t* out, int64_t ld, const int* at, int64_t col0,
+                                         int64_t cols, int wm, int wn, int lane, const AccT<C>& acc) {
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      // (all 64 addresses at once spill)
+      if (v % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+      const int row = at[wm * C::FM * 32 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
+      if (row < 0) continue;
+      uint16_t* const to = out + row * ld;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const int64_t col = col0 + wn * C::FN * 32 + j * 32 + (lane & 31);
+        if (col < cols) to[col] = f32_to_bf16(acc.v[i][j][v]);
+      }
+    }
+}
+
 // Stage a BM x 64 tile of a zero-padded bf16 matrix whose columns
 // c0..c0+63 all exist (row stride a multiple of 8), scaling each element by
 // `scale` in fp32 and rounding back to bf16 when do_scale is set.
@@ -401,13 +433,14 @@ struct FwdArgs {
 };
 
 // Rows of many adapters: row i has the adapter index[i] (none outside 0 ..
-// adapters - 1).  U arrives as fp32 partial sums of X A^T (multi.hip), B and
-// the scales are those of all adapters; U, ldu and s above are not used.
+// adapters - 1).  The tiles take the rows in the order order[0], order[1], ..
+// (within windows of kMultiWindow rows).  s U arrives in that order as fp32 partial sums (multi.hip), B is that of
+// all adapters; U, ldu and s above are not used.
 struct MultiFwdArgs : FwdArgs {
   const float* part;     // [slices][M][ceil(r / 8) * 8], zero-padded
-  int slices;
-  const float* scales;   // [adapters]
+  int slices;            // 8 at most
   const int32_t* index;  // [M]
+  const int32_t* order;  // [M], or null: as they are
   int adapters;
 };
 
@@ -421,104 +454,129 @@ struct MultiFwdArgs : FwdArgs {
 // Zero times an infinity or NaN of another row's adapter would not be zero:
 // such elements of B are staged as zeros and noted, by adapter and column,
 // and the adapter's own rows get NaN in those columns at the end.
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
 template <class C>
 __device__ __forceinline__ void multi_lora(const MultiFwdArgs& p, uint16_t* As, uint16_t* Bs,
-                                           int64_t m0, int64_t n0, int wm, int wn, int lane, int tid,
-                                           AccT<C>& acc) {
+                                           const int* adapter, int64_t m0, int64_t n0, int wm,
+                                           int wn, int lane, int tid, AccT<C>& acc) {
   constexpr int kWaves = C::BM / 64;  // waves that look at the tile's rows
   constexpr int kWords = C::BN / 32;
-  __shared__ __attribute__((aligned(16))) int owner[C::BM];  // adapter, then its place in `list`
-  __shared__ int list[C::BM], place[C::BM];
-  __shared__ int found[kWaves];
+  __shared__ int owner[C::BM];        // a row's adapter, as its place in `list`
+  __shared__ int list[C::BM];
+  __shared__ int wave_list[C::BM], wave_place[C::BM];
+  __shared__ int wave_found[kWaves], found[kWaves];
   __shared__ uint32_t odd[C::BM * kWords];  // columns with an infinity or NaN, by place
   __shared__ int any_odd;
-  int a = -1, lead = tid;
-  if (tid < C::BM) {
-    if (m0 + tid < p.M) a = p.index[m0 + tid];
-    if ((unsigned)a >= (unsigned)p.adapters) a = -1;
-    owner[tid] = a;
+  // The tile's adapters in the order of their first rows: each wave lists
+  // those of its 64 rows, then what earlier waves have not listed is added.
+  const int w = tid >> 6;
+  const int a = w < kWaves ? adapter[tid] : -1;
+  int lead = lane, at = -1;
+  uint64_t mask = 0;  // first rows of an adapter within the wave
+  if (w < kWaves) {
+#pragma unroll 8
+    for (int t = 63; t >= 0; --t)
+      if (__builtin_amdgcn_readlane(a, t) == a) lead = t;
+    mask = __builtin_amdgcn_ballot_w64(a >= 0 && lead == lane);
   }
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+  const bool first = mask >> lane & 1;
+  const int mine = w * 64 + __builtin_popcountll(mask & below);
+  if (first) wave_list[mine] = a;
+  if (w < kWaves && lane == 0) wave_found[w] = __builtin_popcountll(mask);
   for (int e = tid; e < C::BM * kWords; e += C::NT) odd[e] = 0;
   if (tid == 0) any_odd = 0;
   __syncthreads();
-  // the adapters of the tile in the order of their first rows (`lead`)
-  uint64_t mask = 0;
-  if (tid < C::BM) {
-    const int end = (tid | 63) + 1;  // the wave's last row: the same trips in every lane
-    for (int t = 0; t < end; t += 4) {
-      const i32x4 v = *reinterpret_cast<const i32x4*>(owner + t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (v[i] == a && t + i < lead) lead = t + i;
-    }
-    mask = __builtin_amdgcn_ballot_w64(a >= 0 && lead == tid);
-    if (lane == 0) found[tid >> 6] = __builtin_popcountll(mask);
-  }
+  int same = -1;  // the entry of an earlier wave
+  if (first)
+    for (int v = 0; v < w && same < 0; ++v)
+      for (int e = 0; e < wave_found[v] && same < 0; ++e)
+        if (wave_list[64 * v + e] == a) same = 64 * v + e;
+  const uint64_t add = __builtin_amdgcn_ballot_w64(first && same < 0);
+  if (w < kWaves && lane == 0) found[w] = __builtin_popcountll(add);
   __syncthreads();
   int count = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (tid >> 6 == w && (mask >> lane & 1)) {
-      const int at = count + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
+  for (int v = 0; v < kWaves; ++v) {
+    if (v == w && (add >> lane & 1)) {
+      at = count + __builtin_popcountll(add & below);
       list[at] = a;
-      place[tid] = at;
+      wave_place[mine] = at;
     }
-    count += found[w];
+    count += found[v];
   }
   __syncthreads();
-  if (tid < C::BM) owner[tid] = a >= 0 ? place[lead] : -1;
+  if (same >= 0) at = wave_place[same];
+  at = __shfl(at, lead, 64);
+  if (w < kWaves) owner[tid] = a >= 0 ? at : -1;
   __syncthreads();
+
   const int units = (p.r + 7) >> 3, total = count * units;  // units of an adapter, of the tile
   const int64_t ldp = 8 * units;
   const bool bvec = (p.r & 7) == 0;
+  constexpr int NA = C::BM * 8 / C::NT, NB = C::BN * 8 / C::NT;  // 16-byte pieces per thread
+  const int c8 = tid & 7;                                         // of the same unit
   for (int q0 = 0; q0 < total; q0 += 8) {
-    for (int e = tid; e < C::BM * 8; e += C::NT) {
-      const int row = e >> 3, c8 = e & 7, q = q0 + c8;
-      const int ai = q / units;
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      if (q < total && owner[row] == ai) {
-        const float* src = p.part + (m0 + row) * ldp + 8 * (q - ai * units);
-        f32x4 x = *reinterpret_cast<const f32x4*>(src), y = *reinterpret_cast<const f32x4*>(src + 4);
-        for (int s = 1; s < p.slices; ++s) {  // in order
-          src += p.M * ldp;
-          x += *reinterpret_cast<const f32x4*>(src);
-          y += *reinterpret_cast<const f32x4*>(src + 4);
+    const bool in = q0 + c8 < total;
+    const int ai = in ? (q0 + c8) / units : 0, j = in ? 8 * (q0 + c8 - ai * units) : 0;
+    // U: rows of other adapters read what is there and drop it.  (Loads behind
+    // branches, or more of them at once, spill the accumulators.)
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int row = (tid >> 3) + i * (C::NT / 8);
+      const int64_t m = m0 + row < p.M ? m0 + row : p.M - 1;
+      const float* src = p.part + m * ldp + j;
+      f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f}, y = x;
+      for (int s0 = 0; s0 < p.slices; s0 += 4) {
+        f32x4 u[4], v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float* at = src + (s0 + s < p.slices ? s0 + s : 0) * p.M * ldp;
+          u[s] = *reinterpret_cast<const f32x4*>(at);
+          v[s] = *reinterpret_cast<const f32x4*>(at + 4);
         }
-        const float sc = p.scales[list[ai]];
-        v = u32x4{pack_bf16x2(x[0] * sc, x[1] * sc), pack_bf16x2(x[2] * sc, x[3] * sc),
-                  pack_bf16x2(y[0] * sc, y[1] * sc), pack_bf16x2(y[2] * sc, y[3] * sc)};
+#pragma unroll
+        for (int s = 0; s < 4; ++s)  // in order
+          if (s0 + s < p.slices) {
+            x += u[s];
+            y += v[s];
+          }
       }
-      *reinterpret_cast<u32x4*>(As + a_off(row, c8)) = v;
+      const bool has = in && owner[row] == ai;
+      *reinterpret_cast<u32x4*>(As + a_off(row, c8)) =
+          has ? u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
+                      pack_bf16x2(y[2], y[3])}
+              : u32x4{0u, 0u, 0u, 0u};
     }
-    for (int e = tid; e < C::BN * 8; e += C::NT) {
-      const int row = e >> 3, c8 = e & 7, q = q0 + c8;
-      int64_t g = n0 + row;
+    u32x4 bv[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      int64_t g = n0 + (tid >> 3) + i * (C::NT / 8);
       if (g >= p.N) g = p.N - 1;
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      if (q < total) {
-        const int ai = q / units, j = 8 * (q - ai * units);
-        const uint16_t* src = p.B + ((int64_t)list[ai] * p.N + g) * p.r + j;
-        if (bvec) {
-          v = *reinterpret_cast<const u32x4*>(src);
-        } else {
-          uint16_t t[8];
+      const uint16_t* src = p.B + ((int64_t)list[ai] * p.N + g) * p.r + j;
+      if (bvec) {
+        bv[i] = *reinterpret_cast<const u32x4*>(src);
+      } else {
+        uint16_t t[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = j + i < p.r ? src[i] : (uint16_t)0;
+        for (int e = 0; e < 8; ++e) t[e] = j + e < p.r ? src[e] : (uint16_t)0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = (uint32_t)t[2 * i] | ((uint32_t)t[2 * i + 1] << 16);
-        }
-        // bit 15 of a half: its exponent is all ones
-        u32x4 top;
+        for (int e = 0; e < 4; ++e) bv[i][e] = (uint32_t)t[2 * e] | ((uint32_t)t[2 * e + 1] << 16);
+      }
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-        if (top[0] | top[1] | top[2] | top[3]) {
+    for (int i = 0; i < NB; ++i) {
+      const int row = (tid >> 3) + i * (C::NT / 8);
+      u32x4 v = in ? bv[i] : u32x4{0u, 0u, 0u, 0u};
+      // bit 15 of a half: its exponent is all ones
+      u32x4 top;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] &= ~((top[i] >> 15) * 0xffffu);
-          atomicOr(&odd[ai * kWords + (row >> 5)], 1u << (row & 31));
-          any_odd = 1;
-        }
+      for (int e = 0; e < 4; ++e) top[e] = ((v[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+      if (top[0] | top[1] | top[2] | top[3]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] &= ~((top[e] >> 15) * 0xffffu);
+        atomicOr(&odd[ai * kWords + (row >> 5)], 1u << (row & 31));
+        any_odd = 1;
       }
       *reinterpret_cast<u32x4*>(Bs + row * LDA + c8 * 8) = v;
     }
@@ -576,10 +634,36 @@ __global__ __launch_bounds__(C::NT, 1) void k_qgemm_fwd(Args p) {
   const int64_t cblocks = kblocks >> BS;  // constants per weight row
   const __amdgpu_buffer_rsrc_t qrs = bytes_rsrc(p.q8, N * cblocks);
   const __amdgpu_buffer_rsrc_t srs = bytes_rsrc(p.step, 4 * ((N * cblocks + 255) >> 8));
-  const __amdgpu_buffer_rsrc_t xrsrc = rows_rsrc(p.X, K, m0, M);
+  constexpr bool kMulti = std::is_same_v<Args, MultiFwdArgs>;
+  int64_t x0 = m0;  // first row that the resource reaches
+  if constexpr (kMulti)
+    if (p.order) x0 = m0 / kMultiWindow * kMultiWindow;
+  const __amdgpu_buffer_rsrc_t xrsrc = rows_rsrc(p.X, K, x0, M);
+  [[maybe_unused]] int xvoff[C::XLD];  // kMulti: this lane's rows, in order
+  // ... and each row of the tile: where it is, and its adapter
+  __shared__ int row_at[kMulti ? C::BM : 1], adapter[kMulti ? C::BM : 1];
+  if constexpr (kMulti) {
+    if (tid < C::BM) {
+      const int m = m0 + tid >= M ? -1 : p.order ? p.order[m0 + tid] : (int)(m0 + tid);
+      const int a = m < 0 ? -1 : p.index[m];
+      row_at[tid] = m;
+      adapter[tid] = (unsigned)a < (unsigned)p.adapters ? a : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < C::XLD; ++q) {
+      const int r = 8 * (q * (C::NT / 64) + wave) + (lane >> 3);
+      const int64_t m = m0 + r < M ? m0 + r : M - 1;
+      const int64_t gr = p.order ? p.order[m] : m;
+      xvoff[q] = (int)(((gr - x0) * K + ((lane & 7) ^ ((r >> 1) & 7)) * 8) * 2);
+    }
+  }
   auto load_x = [&](uint16_t* As_dst, int64_t kt) {
     if (kt >= kblocks) kt = kblocks - 1;
-    load_rows_lds<C, false>(As_dst, xrsrc, K, m0, M, kt * BK, K, wave, lane);  // K % 64 == 0
+    if constexpr (kMulti) {
+      load_rows_at<C>(As_dst, xrsrc, xvoff, (int)(kt * BK * 2), wave);
+    } else {
+      load_rows_lds<C, false>(As_dst, xrsrc, K, m0, M, kt * BK, K, wave, lane);  // K % 64 == 0
+    }
   };
   // The main loop, for an expanding thread (D: weight row tid of the tile,
   // clamped; rows past N are computed and dropped) or an MFMA-only one.
@@ -706,9 +790,9 @@ __global__ __launch_bounds__(C::NT, 1) void k_qgemm_fwd(Args p) {
   else
     run(std::false_type{});
 
-  if constexpr (std::is_same_v<Args, MultiFwdArgs>) {
-    multi_lora<C>(p, xs0, ws0, m0, n0, wm, wn, lane, tid, acc);
-    store_tile<C>(p.Y, N, m0, n0, M, N, wm, wn, lane, acc);
+  if constexpr (kMulti) {
+    multi_lora<C>(p, xs0, ws0, adapter, m0, n0, wm, wn, lane, tid, acc);
+    store_at<C>(p.Y, N, row_at, n0, N, wm, wn, lane, acc);
     return;
   }
   // LoRA: extra contraction over r with A-side bf16(s U) and B-side B.
@@ -966,10 +1050,10 @@ template <class C>
 #ifdef QN_QGEMM_MULTI
 hipError_t launch_qgemm_multi_fwd(const Nf4View& w, const uint16_t* X, int64_t M,
                                   const float* part, int slices, const uint16_t* B, int32_t r,
-                                  const float* scales, int adapters, const int32_t* index,
+                                  int adapters, const int32_t* index, const int32_t* order,
                                   uint16_t* Y, hipStream_t stream) {
   const MultiFwdArgs a{{X, w.codes, w.q8, w.step, nullptr, 0, B, r, 0.0f, Y, M, w.N, w.K, w.ut},
-                       part, slices, scales, index, adapters};
+                       part, slices, index, order, adapters};
   return small_tiles(M, w.N) ? launch_fwd<SmallCfg>(a, w, M, stream)
                              : launch_fwd<GemmCfg>(a, w, M, stream);
 }

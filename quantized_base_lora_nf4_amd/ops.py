@@ -339,48 +339,6 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     return dX, dA, dB
 
 
-def multi_workspace_size(M: int, N: int, K: int, r: int) -> int:
-    return int(lib().qlora_multi_workspace_size(M, N, K, r))
-
-
-def qlora_linear_multi_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
-                           s: torch.Tensor, index: torch.Tensor, Y: Optional[torch.Tensor] = None,
-                           ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Rows of many adapters over one frozen weight:
-    Y_i = X_i W^T + s_a (X_i A_a^T) B_a^T with a = index[i], and X_i W^T where
-    index[i] is not one of 0 .. n - 1.
-
-    X [M, K], A [n, r, K], B [n, N, r] bf16 (adapters of smaller rank padded
-    with zeros), s [n] float32, index [M] int32, all on the weight's GPU.  Rows
-    may come in any order.  Kernels and buffers run on that GPU's current stream
-    unless one is given."""
-    dev = _check_weight(w)
-    for name, t, nd in (("X", X, 2), ("A", A, 3), ("B", B, 3)):
-        if not isinstance(t, torch.Tensor) or t.dim() != nd:
-            raise ValueError(f"{name} must be {nd}-D")
-    M, (n, r) = X.shape[0], A.shape[:2]
-    _check_tensors([("codes", w.codes, w.codes.shape, False), ("q8", w.q8, w.q8.shape, False),
-                    ("step", w.step, w.step.shape, False),
-                    ("X", X, (M, w.K), True), ("A", A, (n, r, w.K), True),
-                    ("B", B, (n, w.N, r), True), ("s", s, (n,), False),
-                    ("index", index, (M,), False), ("Y", Y, (M, w.N), True)], dev)
-    if s.dtype != torch.float32 or index.dtype != torch.int32:
-        raise TypeError("s must be float32, index int32")
-    # (the weight's device may not be the current one)
-    with torch.cuda.device(dev):
-        st = _stream_obj(stream)
-        with torch.cuda.stream(st):
-            if Y is None:
-                Y = torch.empty(M, w.N, dtype=torch.bfloat16, device=dev)
-            ws = _workspace(multi_workspace_size(M, w.N, w.K, r), dev, ws)
-            s_ = w.struct()
-            rc = lib().qlora_linear_multi_fwd(ctypes.byref(s_), _ptr(X), M, _ptr(A), _ptr(B), _ptr(s),
-                                              n, r, _ptr(index), _ptr(Y), _ptr(ws),
-                                              ws.numel() * ws.element_size(), st.cuda_stream)
-    check(rc, "qlora_linear_multi_fwd")
-    return Y
-
-
 LQ_START = {"svd": 0, "quantize": 1}
 
 
@@ -514,46 +472,4 @@ class QLoRALinear(torch.nn.Module):
     def forward(self, X):
         shp = X.shape
         Y = QLoRALinearFunction.apply(X.reshape(-1, shp[-1]), self.A, self.B, self.nf4, self.s)
-        return Y.reshape(*shp[:-1], Y.shape[-1])
-
-
-class QLoRAMultiLinear(torch.nn.Module):
-    """A frozen NF4 weight with `slots` places for LoRA pairs of rank up to r,
-    for rows that each use one of them (serving what QLoRALinear trained; no
-    gradients).  The weight is a QLoRALinear's (shared, not copied) or an
-    NF4Weight."""
-
-    def __init__(self, base, slots: int, r: int):
-        super().__init__()
-        self.nf4 = base.nf4 if isinstance(base, QLoRALinear) else base
-        dev = self.nf4.codes.device
-        self.register_buffer("A", torch.zeros(slots, r, self.nf4.K, dtype=torch.bfloat16, device=dev))
-        self.register_buffer("B", torch.zeros(slots, self.nf4.N, r, dtype=torch.bfloat16, device=dev))
-        self.register_buffer("scales", torch.zeros(slots, dtype=torch.float32, device=dev))
-
-    @torch.no_grad()
-    def put(self, slot: int, A: torch.Tensor, B: torch.Tensor, s: float) -> None:
-        """Copy an adapter (A [k, K], B [N, k], k <= r) with its scale into a slot."""
-        slots, r, K = self.A.shape
-        if not 0 <= slot < slots:
-            raise ValueError(f"slot {slot} is not one of {slots}")
-        k = A.shape[0]
-        if k > r or A.shape != (k, K) or B.shape != (self.nf4.N, k):
-            raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} do not fit rank {r} beside a "
-                             f"{self.nf4.N} x {K} weight")
-        self.A[slot].zero_()[:k] = A
-        self.B[slot].zero_()[:, :k] = B
-        self.scales[slot] = s
-
-    def load(self, slot: int, layer: QLoRALinear) -> None:
-        """Copy the adapter of a QLoRALinear into a slot."""
-        self.put(slot, layer.A, layer.B, layer.s)
-
-    @torch.no_grad()
-    def forward(self, X, index):
-        """X [..., K] bf16, index int32 of X's leading shape: the slot of each
-        row, -1 for none."""
-        shp = X.shape
-        Y = qlora_linear_multi_fwd(self.nf4, X.reshape(-1, shp[-1]).contiguous(), self.A, self.B,
-                                   self.scales, index.reshape(-1).contiguous())
         return Y.reshape(*shp[:-1], Y.shape[-1])

@@ -5,7 +5,8 @@ Tolerance per output, with u = 2^-8 (half a bf16 step): Y is rounded once
 (u |Y|).  Up to 16 rows the weight enters as level times constant, levels
 rounded to bf16 (u) instead of the product (u): 2 u of sum |x w| at most, and
 independent from weight to weight, so 8 deviations of u sqrt(sum (x w)^2).  Other rows round
-s U once (u of sum |s u b| at most, independent over the rank likewise).
+s U once (u of sum |s u b| at most, independent over the rank likewise).  Which
+of the two a batch meets is the kernels' choice: both are counted.
 Sums are fp32: 2^-24 per addition, K + r of them at most, of sum |x w| + ...;
 both are far below the budget: 2^-16 of the sum of magnitudes is added.
 """
@@ -81,7 +82,7 @@ def spread(M, n, how, seed=0):
 
 
 @pytest.mark.parametrize("how", ["each", "runs", "random", "one", "none"])
-@pytest.mark.parametrize("M", [1, 2, 7, 16, 17, 33, 64, 65, 129, 300])
+@pytest.mark.parametrize("M", [1, 2, 7, 16, 17, 32, 33, 64, 65, 129, 300, 4097, 8300])
 def test_rows_and_orders(M, how):
     say(f"[multi] {M} rows, {how}")
     w, A, B, s = make(264, 320, 9, 16)
@@ -89,7 +90,7 @@ def test_rows_and_orders(M, how):
     check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [3, 40, 260])
+@pytest.mark.parametrize("M", [3, 40, 4100])
 @pytest.mark.parametrize("r", [1, 4, 8, 9, 16, 24, 33, 64, 100, 128, 256])
 def test_ranks(M, r):
     say(f"[multi] {M} rows, rank {r}")
@@ -98,7 +99,7 @@ def test_ranks(M, r):
     check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [1, 5, 16, 50, 400])
+@pytest.mark.parametrize("M", [1, 5, 16, 50, 700])
 @pytest.mark.parametrize("N,K", [(8, 64), (16, 64), (1024, 64), (8, 2048), (520, 1088), (2048, 512), (28672, 512)])
 def test_sizes(M, N, K):
     say(f"[multi] {M} rows, {N} x {K}")
@@ -107,7 +108,7 @@ def test_sizes(M, N, K):
     check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [4, 100])
+@pytest.mark.parametrize("M", [4, 30, 100, 4100])
 @pytest.mark.parametrize("code,blocksize", [("nf4", 128), ("nf4", 256), ("fp4", 64), ("nf3", 64), ("nf2", 128), ("user4", 64)])
 def test_code_types(M, code, blocksize):
     say(f"[multi] {code}, blocks of {blocksize}")
@@ -117,14 +118,24 @@ def test_code_types(M, code, blocksize):
     check("Y", Y, w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [16, 64, 300])
+@pytest.mark.parametrize("M", [16, 64, 300, 4100])
 def test_many_adapters(M):
     """More adapters than rows, and as many adapters as rows."""
-    for n in (500, M):
+    for n in (5000, M):
         w, A, B, s = make(72, 128, n, 16)
         X = rows(M, 128)
         index = torch.randperm(n, generator=torch.Generator().manual_seed(3))[:M].to(torch.int32).cuda()
         check(f"{n}", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
+
+
+def test_wide_rows_are_taken_as_they_come():
+    """Rows so wide that a window of them is past 32-bit offsets: no order."""
+    K = 1 << 18
+    w, A, B, s = make(8, K, 3, 8)
+    X, index = rows(5000, K), spread(5000, 3, "random")
+    Y = qn.qlora_linear_multi_fwd(w, X, A, B, s, index)
+    some = torch.randperm(5000, generator=torch.Generator().manual_seed(1))[:200].cuda()
+    check("200 rows", Y[some], w, X[some].contiguous(), A, B, s, index[some])
 
 
 def test_large_few_token_rows():
@@ -134,7 +145,7 @@ def test_large_few_token_rows():
     check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [1, 16, 17, 300])
+@pytest.mark.parametrize("M", [1, 16, 17, 4100])
 def test_one_adapter_is_the_layer(M):
     """All rows of one adapter: the layer's own forward within the roundings of
     U (it rounds U and s U, this s U or nothing)."""
@@ -145,10 +156,15 @@ def test_one_adapter_is_the_layer(M):
     assert float((Y.double() - Z.double()).norm() / Z.double().norm()) <= U
     none = qn.qlora_linear_multi_fwd(w, X, A, B, s, spread(M, 4, "none"))
     base = qn.qlora_linear_fwd(w, X, torch.zeros_like(A[0]), torch.zeros_like(B[0]), 1.0)
-    assert torch.equal(none, base)
+    # without an adapter both are X W^T: the same kernels but for batches whose
+    # weight enters as level times constant here alone
+    if M == 17:
+        assert float((none.double() - base.double()).norm() / base.double().norm()) <= U
+    else:
+        assert torch.equal(none, base)
 
 
-@pytest.mark.parametrize("M", [5, 16, 70, 300])
+@pytest.mark.parametrize("M", [5, 16, 20, 70, 4100])
 def test_rows_do_not_see_other_adapters(M):
     """NaN and infinities in other rows and other adapters, in adapter 0 and in
     unused ones, change nothing."""
@@ -173,19 +189,21 @@ def test_rows_do_not_see_other_adapters(M):
 
 def test_wrong_indices_are_no_adapter():
     w, A, B, s = make(64, 128, 3, 8)
-    for M in (9, 40):
+    for M in (9, 40, 4500):
         X = rows(M, 128)
-        index = torch.tensor([0, 3, -1, 2 ** 31 - 1, -2 ** 31, 1, 2, 1000, -7] * 5, dtype=torch.int32)[:M].cuda()
+        index = torch.tensor([0, 3, -1, 2 ** 31 - 1, -2 ** 31, 1, 2, 1000, -7] * 500, dtype=torch.int32)[:M].cuda()
         Y = qn.qlora_linear_multi_fwd(w, X, A, B, s, index)
         check("Y", Y, w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [6, 200])
+@pytest.mark.parametrize("M", [6, 20, 200, 4100])
 def test_order_of_rows(M):
     """A row's result does not depend on where it stands or on its neighbours."""
     w, A, B, s = make(136, 256, 6, 24)
     X, index = rows(M, 256), spread(M, 6, "random")
     Y = qn.qlora_linear_multi_fwd(w, X, A, B, s, index)
+    # (windows of 4096 rows are put in order one by one: across them, sums stay
+    # in their places too)
     p = torch.randperm(M, generator=torch.Generator().manual_seed(1)).cuda()
     assert torch.equal(qn.qlora_linear_multi_fwd(w, X[p].contiguous(), A, B, s, index[p].contiguous()), Y[p])
     assert torch.equal(qn.qlora_linear_multi_fwd(w, X, A, B, s, index), Y)
@@ -203,13 +221,13 @@ def test_pool_past_32_bits():
     for a in (0, n - 1):
         A[a] = (torch.randn(r, K, generator=g, device="cuda") * K ** -0.5).to(BF)
         B[a] = torch.randn(N, r, generator=g, device="cuda").to(BF)
-    for M in (5, 60):
+    for M in (5, 60, 700):
         X = rows(M, K)
         index = torch.where(torch.arange(M) % 2 == 0, n - 1, 0).to(torch.int32).cuda()
         check(f"{M}", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
-@pytest.mark.parametrize("M", [8, 90])
+@pytest.mark.parametrize("M", [8, 90, 4100])
 def test_captured_with_new_adapters(M):
     w, A, B, s = make(136, 256, 6, 16)
     X, index = rows(M, 256), spread(M, 6, "random")
@@ -231,7 +249,7 @@ def test_captured_with_new_adapters(M):
 
 def test_other_stream_workspace_and_output():
     w, A, B, s = make(136, 256, 6, 16)
-    for M in (8, 90):
+    for M in (8, 90, 4100):
         X, index = rows(M, 256), spread(M, 6, "random")
         Y = qn.qlora_linear_multi_fwd(w, X, A, B, s, index)
         torch.cuda.synchronize()
@@ -284,11 +302,11 @@ def test_module():
     (dict(A=lambda t: t[0]), ValueError, "A must be 3-D"),
     (dict(B=lambda t: t[:2]), ValueError, "B has shape"),
     (dict(B=lambda t: t[:, :64]), ValueError, "B has shape"),
-    (dict(A=lambda t: t.float()), TypeError, "A must be bf16"),
+    (dict(A=lambda t: t.float()), TypeError, "A has dtype"),
     (dict(s=lambda t: t[:2]), ValueError, "s has shape"),
-    (dict(s=lambda t: t.double()), TypeError, "s must be float32"),
+    (dict(s=lambda t: t.double()), TypeError, "s has dtype"),
     (dict(index=lambda t: t[:4]), ValueError, "index has shape"),
-    (dict(index=lambda t: t.long()), TypeError, "index int32"),
+    (dict(index=lambda t: t.long()), TypeError, "index has dtype"),
     (dict(index=lambda t: t.cpu()), ValueError, "index is on cpu"),
     (dict(X=lambda t: t.cpu()), ValueError, "X is on cpu"),
     (dict(X=lambda t: torch.cat([t, t], 1)[:, :128]), ValueError, "contiguous"),
