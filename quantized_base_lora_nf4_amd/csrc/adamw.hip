@@ -60,26 +60,29 @@ struct __attribute__((packed, aligned(sizeof(E)))) Loose {
   uint32_t w[W * sizeof(E) / 4];
 };
 
-// W elements at p (aligned to their type) as floats; the first n of them exist.
+// W elements at p (aligned to their type) as they are; the first n of them
+// exist, the others are zeros.
 template <class E, int W>
-__device__ __forceinline__ void load(float (&x)[W], const E* p, int n) {
+__device__ __forceinline__ void load(Loose<E, W>& x, const E* p, int n) {
   if (n >= W) {
-    const Loose<E, W> v = *reinterpret_cast<const Loose<E, W>*>(p);
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if constexpr (sizeof(E) == 4) x[i] = word_to_f32(v.w[i]);
-      else x[i] = i & 1 ? bf16_hi_to_f32(v.w[i >> 1]) : bf16_lo_to_f32(v.w[i >> 1]);
-    }
+    x = *reinterpret_cast<const Loose<E, W>*>(p);
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      x[i] = 0.0f;
-      if (i < n) {
-        if constexpr (sizeof(E) == 4) x[i] = p[i];
-        else x[i] = bf16_to_f32(p[i]);
+    for (int i = 0; i < W * (int)sizeof(E) / 4; ++i) {
+      x.w[i] = 0;
+      if constexpr (sizeof(E) == 4) {
+        if (i < n) x.w[i] = __builtin_bit_cast(uint32_t, p[i]);
+      } else {
+        if (2 * i < n) x.w[i] = p[2 * i];
+        if (2 * i + 1 < n) x.w[i] |= (uint32_t)p[2 * i + 1] << 16;
       }
     }
   }
+}
+template <class E, int W>
+__device__ __forceinline__ float element(const Loose<E, W>& x, int i) {
+  if constexpr (sizeof(E) == 4) return word_to_f32(x.w[i]);
+  else return i & 1 ? bf16_hi_to_f32(x.w[i >> 1]) : bf16_lo_to_f32(x.w[i >> 1]);
 }
 
 template <class E, int W>
@@ -124,19 +127,21 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
 // ... and the factor that maps it to the largest code's power.
 __device__ __forceinline__ float factor_of(float s, float top) { return s > 0.0f ? top / s : 0.0f; }
 
-// Codes.  y is at most one rounding above the largest code's power.
+// The code of a value whose power is y (at most one rounding above the largest
+// code's; a NaN counts as 0): the guess from a root that is within a few units
+// in the last place is the code or one less.
 __device__ __forceinline__ float code_m(float y) {
 #pragma clang fp contract(off)
-  float n = floorf(__builtin_amdgcn_sqrtf(y) + 0.4999f);  // the code or one less
+  const float n = floorf(__builtin_amdgcn_sqrtf(y) + 0.4999f);
   const float h = n + 0.5f;
-  return h * h <= y ? n + 1.0f : n;
+  return h * h <= y ? h + 0.5f : n;
 }
-__device__ __forceinline__ float code_v(float y) {
+// root: the square root of y, within a few units (0 for y below 2^-96: code 0 or 1).
+__device__ __forceinline__ float code_v(float y, float root) {
 #pragma clang fp contract(off)
-  float n = floorf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(y)) + 0.4999f);
-  float h = n + 0.5f;
-  h = h * h;  // exact
-  return h * h <= y ? n + 1.0f : n;
+  const float n = floorf(__builtin_amdgcn_sqrtf(root) + 0.4999f);
+  const float h = n + 0.5f, h2 = h * h;  // exact
+  return h2 * h2 <= y ? h + 0.5f : n;
 }
 __device__ __forceinline__ float value_m(float c, float s) {
 #pragma clang fp contract(off)
@@ -188,44 +193,69 @@ __device__ __forceinline__ Step step_of(const AdamHyper& h) {
   return s;
 }
 
-// One block of one tensor: p, g (and c) at the block's first element, of
-// which `count` exist; block `blk` of the states.
+// What a lane loads of a block: 8 elements, as J vectors of W.  fp32 data moves
+// as 4 elements per lane and access, so that 32 lanes read whole lines; 16- and
+// 8-bit data alone as 8.
 template <bool k8, class PT, class GT>
-__device__ __forceinline__ void update_block(PT* p, const GT* g, uint16_t* c, const State& st,
-                                             int64_t blk, int count, const Step& s) {
-  // fp32 data moves as 4 elements per lane and access, so that 32 lanes read
-  // whole lines; 16- and 8-bit data alone as 8.
-  constexpr int W = k8 && sizeof(PT) == 2 && sizeof(GT) == 2 ? 8 : 4;
-  constexpr int J = 8 / W;
-  const int lane = threadIdx.x & 31;
-  float gv[J][W], pv[J][W], m[J][W], v[J][W];
-  int n[J];
-  Codes<W> cm[J], cv[J];
-  float ms = 0.0f, vs = 0.0f;
+struct Raw {
+  static constexpr int W = k8 && sizeof(PT) == 2 && sizeof(GT) == 2 ? 8 : 4, J = 8 / W;
+  Loose<GT, W> g[J];
+  Loose<PT, W> p[J];
+  Codes<W> cm[k8 ? J : 1], cv[k8 ? J : 1];
+  f32x4 m[k8 ? 1 : J], v[k8 ? 1 : J];
+  float ms, vs;
+
+  // p, g at the block's first element, of which `count` exist; block `blk` of
+  // the states
+  __device__ __forceinline__ void load_block(const PT* pp, const GT* gp, const State& st, int64_t blk,
+                                             int count) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = j * 32 * W + lane * W;
-    n[j] = count - e;
-    load<GT, W>(gv[j], g + e, n[j]);
-    load<PT, W>(pv[j], p + e, n[j]);
+    for (int j = 0; j < J; ++j) {
+      const int e = j * 32 * W + lane * W;
+      load<GT, W>(g[j], gp + e, count - e);
+      load<PT, W>(p[j], pp + e, count - e);
+      if constexpr (k8) {
+        cm[j] = *reinterpret_cast<const Codes<W>*>((const uint8_t*)st.m + blk * kBlock + e);
+        cv[j] = *reinterpret_cast<const Codes<W>*>((const uint8_t*)st.v + blk * kBlock + e);
+      } else {
+        m[j] = *reinterpret_cast<const f32x4*>((const float*)st.m + blk * kBlock + e);
+        v[j] = *reinterpret_cast<const f32x4*>((const float*)st.v + blk * kBlock + e);
+      }
+    }
     if constexpr (k8) {
-      cm[j] = *reinterpret_cast<const Codes<W>*>((const uint8_t*)st.m + blk * kBlock + e);
-      cv[j] = *reinterpret_cast<const Codes<W>*>((const uint8_t*)st.v + blk * kBlock + e);
-    } else {
-      load<float, W>(m[j], (const float*)st.m + blk * kBlock + e, W);
-      load<float, W>(v[j], (const float*)st.v + blk * kBlock + e, W);
+      ms = st.ms[blk];
+      vs = st.vs[blk];
     }
   }
-  if constexpr (k8) {
-    ms = st.ms[blk];
-    vs = st.vs[blk];
+};
+
+// The step of one block.
+template <bool k8, class PT, class GT>
+__device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, uint16_t* c,
+                                             const State& st, int64_t blk, int count,
+                                             const Step& s) {
+  constexpr int W = Raw<k8, PT, GT>::W, J = Raw<k8, PT, GT>::J;
+  const int lane = threadIdx.x & 31;
+  float gv[J][W], pv[J][W], m[J][W], v[J][W], root[J][W];
+  int n[J];
+  Codes<W> cm[J], cv[J];
+  float ms, vs;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+  for (int j = 0; j < J; ++j) {
+    n[j] = count - (j * 32 * W + lane * W);
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        m[j][i] = value_m(byte_f32(cm[j].w[i >> 2] ^ 0x80808080u, i & 3) - 128.0f, ms);
-        v[j][i] = value_v(byte_f32(cv[j].w[i >> 2], i & 3), vs);
+    for (int i = 0; i < W; ++i) {
+      gv[j][i] = element(r.g[j], i);
+      pv[j][i] = element(r.p[j], i);
+      if constexpr (k8) {
+        m[j][i] = value_m(byte_f32(r.cm[j].w[i >> 2] ^ 0x80808080u, i & 3) - 128.0f, r.ms);
+        v[j][i] = value_v(byte_f32(r.cv[j].w[i >> 2], i & 3), r.vs);
+      } else {
+        m[j][i] = r.m[j][i];
+        v[j][i] = r.v[j][i];
       }
+    }
   }
   uint32_t mtop = 0, vtop = 0;
 #pragma unroll
@@ -245,7 +275,8 @@ __device__ __forceinline__ void update_block(PT* p, const GT* g, uint16_t* c, co
         vtop = vtop > b ? vtop : b;
       }
       // v_sqrt and v_rcp are within 1 ulp: far below the parameter's rounding
-      const float d = __builtin_amdgcn_sqrtf(v[j][i]) * s.rb2 + s.eps;
+      root[j][i] = __builtin_amdgcn_sqrtf(v[j][i]);
+      const float d = root[j][i] * s.rb2 + s.eps;
       pv[j][i] = pv[j][i] * s.keep - s.lr1 * m[j][i] * __builtin_amdgcn_rcpf(d);
     }
 #pragma unroll
@@ -258,13 +289,14 @@ __device__ __forceinline__ void update_block(PT* p, const GT* g, uint16_t* c, co
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = j * 32 * W + lane * W;
-      store<float, W>((float*)st.m + blk * kBlock + e, m[j], W);
-      store<float, W>((float*)st.v + blk * kBlock + e, v[j], W);
+      *reinterpret_cast<f32x4*>((float*)st.m + blk * kBlock + e) = f32x4{m[j][0], m[j][1], m[j][2], m[j][3]};
+      *reinterpret_cast<f32x4*>((float*)st.v + blk * kBlock + e) = f32x4{v[j][0], v[j][1], v[j][2], v[j][3]};
     }
   } else {
     ms = scale_of(half_max(mtop));
     vs = scale_of(half_max(vtop));
     const float fm = factor_of(ms, 16129.0f), fv = factor_of(vs, 4228250625.0f);
+    const float rv = __builtin_amdgcn_sqrtf(fv), least = fv > 0.0f ? 1.0f : 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = j * 32 * W + lane * W;
@@ -274,9 +306,11 @@ __device__ __forceinline__ void update_block(PT* p, const GT* g, uint16_t* c, co
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = m[j][4 * q + i], y = v[j][4 * q + i];
-          const float a = fm > 0.0f ? code_m(fabsf(x) * fm) : 0.0f;
-          float b = fv > 0.0f ? code_v(y * fv) : 0.0f;
-          if (fv > 0.0f && y > 0.0f && b < 1.0f) b = 1.0f;
+          // A factor of 0, also that of a NaN scale, gives code 0: the median
+          // with a NaN is the lowest of the others.
+          const float a = code_m(__builtin_amdgcn_fmed3f(fabsf(x) * fm, 0.0f, 65536.0f));
+          const float c = code_v(__builtin_amdgcn_fmed3f(y * fv, 0.0f, 0x1p+36f), root[j][4 * q + i] * rv);
+          const float b = __builtin_amdgcn_fmed3f(c, y > 0.0f ? least : 0.0f, 255.0f);
           wm = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_copysignf(a, x) + 128.0f, i, wm);
           wv = __builtin_amdgcn_cvt_pk_u8_f32(b, i, wv);
         }
@@ -293,6 +327,27 @@ __device__ __forceinline__ void update_block(PT* p, const GT* g, uint16_t* c, co
   }
 }
 
+// The chunks k0 .. k1 - 1 of one tensor, of `blocks` blocks, the last of which
+// has `tail` elements.  The next chunk's loads are in flight under the
+// arithmetic of this one.
+template <bool k8, class PT, class GT>
+__device__ __forceinline__ void update_chunks(PT* p, const GT* g, uint16_t* c, const State& st,
+                                              int64_t first, int64_t k0, int64_t k1, int64_t blocks,
+                                              int tail, const Step& s) {
+  const auto size_of = [&](int64_t b) { return b == blocks - 1 ? tail : kBlock; };
+  int64_t b = k0 * kChunk + (threadIdx.x >> 5);  // this half wave's block of each chunk
+  const int64_t end = k1 * kChunk < blocks ? k1 * kChunk : blocks;
+  Raw<k8, PT, GT> a, n;
+  if (b < end) a.load_block(p + b * kBlock, g + b * kBlock, st, first + b, size_of(b));
+  while (b < end) {
+    const int64_t nb = b + kChunk;
+    if (nb < end) n.load_block(p + nb * kBlock, g + nb * kBlock, st, first + nb, size_of(nb));
+    update_block<k8>(a, p + b * kBlock, c ? c + b * kBlock : nullptr, st, first + b, size_of(b), s);
+    a = n;
+    b = nb;
+  }
+}
+
 template <bool k8, bool kCopy, class Tb>
 __global__ __launch_bounds__(kNT) void k_adamw(Tb tb, State st, AdamHyper hyper) {
   const Step s = step_of(hyper);
@@ -306,35 +361,31 @@ __global__ __launch_bounds__(kNT) void k_adamw(Tb tb, State st, AdamHyper hyper)
     if (tb.end[m] > ch) hi = m;
     else lo = m + 1;
   }
-  const int mine = threadIdx.x >> 5;  // this half wave's block of each chunk
-  for (; ch < che; ++ch) {
-    while (tb.end[lo] <= ch) ++lo;
-    const uint32_t k = ch - (lo ? tb.end[lo - 1] : 0u);
+  for (; ch < che; ++lo) {
+    const uint32_t from = lo ? tb.end[lo - 1] : 0u, upto = tb.end[lo];
     const uint32_t tail = tb.tail[lo];
-    const bool last = ch + 1 == tb.end[lo];
-    const int blocks = last ? (int)(tail & 7u) + 1 : kChunk;
-    if (mine >= blocks) continue;
-    const int64_t b = (int64_t)k * kChunk + mine, e = b * kBlock;
-    const int count = last && mine == blocks - 1 ? (int)((tail >> 3) & 255u) + 1 : kBlock;
-    const int64_t blk = (int64_t)tb.first[lo] + b;
+    const int64_t k0 = ch - from, k1 = (che < upto ? che : upto) - from;
+    const int64_t blocks = (int64_t)(upto - from - 1) * kChunk + (tail & 7u) + 1;
+    const int last = (int)((tail >> 3) & 255u) + 1;
     uint16_t* c = nullptr;
-    if constexpr (kCopy)
-      if (tb.c[lo]) c = tb.c[lo] + e;
+    if constexpr (kCopy) c = tb.c[lo];
     const void* g = tb.g[lo];
     void* p = tb.p[lo];
+    const int64_t first = tb.first[lo];
     switch (tail >> 30) {
       case 0:
-        update_block<k8>((uint16_t*)p + e, (const uint16_t*)g + e, c, st, blk, count, s);
+        update_chunks<k8>((uint16_t*)p, (const uint16_t*)g, c, st, first, k0, k1, blocks, last, s);
         break;
       case 1:
-        update_block<k8>((uint16_t*)p + e, (const float*)g + e, c, st, blk, count, s);
+        update_chunks<k8>((uint16_t*)p, (const float*)g, c, st, first, k0, k1, blocks, last, s);
         break;
       case 2:
-        update_block<k8>((float*)p + e, (const uint16_t*)g + e, c, st, blk, count, s);
+        update_chunks<k8>((float*)p, (const uint16_t*)g, c, st, first, k0, k1, blocks, last, s);
         break;
       default:
-        update_block<k8>((float*)p + e, (const float*)g + e, c, st, blk, count, s);
+        update_chunks<k8>((float*)p, (const float*)g, c, st, first, k0, k1, blocks, last, s);
     }
+    ch = from + (uint32_t)k1;
   }
 }
 
