@@ -72,7 +72,7 @@ struct Owners {
   const int32_t* index;  // [M]: adapter of each row
   int adapters;          // index outside 0 .. adapters - 1: none
 };
-__device__ __forceinline__ int owner_of(const Owners& o, int64_t row) {
+[[maybe_unused]] __device__ __forceinline__ int owner_of(const Owners& o, int64_t row) {
   const int a = o.index[row];
   return (unsigned)a < (unsigned)o.adapters ? a : -1;
 }
@@ -201,6 +201,9 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(G == 1 
 void k_qgemv(Args p) {
   constexpr int NT = 64 * KW;
   constexpr bool kMulti = std::is_same_v<Args, MultiGemvArgs>;
+  // rows of many adapters: levels nearer to bf16 values (level_factor)
+  [[maybe_unused]] constexpr float kUp = kMulti ? level_factor<CT>() : 1.0f;
+  [[maybe_unused]] constexpr float kDown = 1.0f / kUp;
   extern __shared__ float lds[];
   uint32_t* lut = reinterpret_cast<uint32_t*>(lds);
   float* ush = lds + kLutWords;
@@ -437,7 +440,8 @@ void k_qgemv(Args p) {
       const int64_t row = e / kblocks, kb = e - row * kblocks;
       const int64_t n = n0 + row < N ? n0 + row : N - 1;
       const int64_t ci = n * cblocks + (kb >> bs);
-      chat_t[row * kbs + kb] = (float)p.q8[ci] * p.step[ci >> 8];
+      if constexpr (kMulti) chat_t[row * kbs + kb] = (float)p.q8[ci] * (p.step[ci >> 8] * kDown);
+      else chat_t[row * kbs + kb] = (float)p.q8[ci] * p.step[ci >> 8];
     }
   } else {
     // The workgroup's constants are the contiguous q8 range starting at
@@ -474,6 +478,7 @@ void k_qgemv(Args p) {
         const int o = qbase + 16 * (c < nchunk ? c : nchunk - 1);
         qv[j] = __builtin_amdgcn_raw_buffer_load_b128(qrs, c < nchunk ? o : kPastEnd, 0, 0);
         st[j] = p.step[o >> 8 < glast ? o >> 8 : glast];
+        if constexpr (kMulti) st[j] *= kDown;
       }
       if (kLateFirst && cp == 0) issue_first();
 #pragma unroll
@@ -508,10 +513,14 @@ void k_qgemv(Args p) {
     // entries b = t / 16 + 32 i, whose low code t / 16 % 16 is the same for
     // every i and whose high code t / 256 + 2 i is uniform over the wave
     static_assert(NT == 512 && kLutWords == 8 * NT, "table split assumes 8 waves");
-    const float lo = level_of<CT>(p.ut, (tid >> 4) & 15);
+    const auto level = [&](int c) {
+      if constexpr (kMulti) return level_of<CT>(p.ut, c) * kUp;
+      else return level_of<CT>(p.ut, c);
+    };
+    const float lo = level((tid >> 4) & 15);
     const int hi0 = __builtin_amdgcn_readfirstlane(tid >> 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lut[tid + NT * i] = pack_bf16x2(lo, level_of<CT>(p.ut, hi0 + 2 * i));
+    for (int i = 0; i < 8; ++i) lut[tid + NT * i] = pack_bf16x2(lo, level(hi0 + 2 * i));
   }
   if (tid < ur) {
     float u = 0.0f;  // slices in order (those past us are zeros)

@@ -53,6 +53,19 @@ hipError_t launch_qgemv(const Nf4View& w, const uint16_t* X, int64_t M, const ui
                         const uint16_t* B, int32_t r, float s, uint16_t* Y, uint16_t* U_out,
                         float* upart, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
 
+// Levels in bf16 under an fp32 constant: with every level times this factor,
+// and the constants divided by it, the levels fall nearer to bf16 values (NF4:
+// rms error 6.3e-4 of the levels' rms instead of 1.06e-3; found by trying
+// multiples of 2^-12 from 1 to 2).
+template <class CT>
+constexpr float level_factor() {
+  if constexpr (CT::kUser) return 1.0f;
+  else return CT::kId == CodeNF4::kId   ? 1.43701171875f
+              : CT::kId == CodeNF3::kId ? 1.781005859375f
+              : CT::kId == CodeNF2::kId ? 1.15625f
+                                        : 1.0078125f;
+}
+
 // ---- rows of many adapters (qgemm_multi.hip, qgemv_multi.hip, qrows.hip, multi.hip) ----
 // Row i has the adapter index[i] (device; none outside 0 .. adapters - 1); A
 // [adapters, r, K], B [adapters, N, r], scales [adapters] fp32.

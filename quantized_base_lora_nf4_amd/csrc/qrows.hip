@@ -10,7 +10,7 @@
 // code word.  Every workgroup reads all of X (from L2; G = 2 halves that
 // traffic), so it comes in the order of the MFMA operands, 1 KB per load, as
 // the down products write it: read in rows, whose fragments put neighbouring
-// lanes 2 K bytes apart, 64 rows took 47 instead of TODO us.  More tokens make
+// lanes 2 K bytes apart, 64 rows over 8192 x 8192 took 47 instead of 29 us.  More tokens make
 // more workgroups (grid dimension y), which find the weight in the caches.
 //
 // The LoRA term is added in the epilogue from U = X A^T (multi.hip), summed
@@ -18,6 +18,12 @@
 // adapter rows of its own token, so adapters never meet.
 //
 // Operand layout and double steps: see gemv.hip.
+//
+// Measured, 64 rows over 8192 x 8192: 27 us (the weight alone: 7 us at a large
+// copy's rate), of which about 8 before and after the loop.  The loop is bound
+// by X: 256 workgroups read 1 MB each, 16 TB/s out of the L2s.  With X and codes
+// from one place (all hits) it takes 9 us instead of 18; without the table
+// lookups, or with the chains of a step one after the other, the same 18.
 #include "kernels.hpp"
 
 namespace qn {
@@ -124,9 +130,15 @@ void k_qrows(RowsArgs p) {
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[g][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // One step as 2 G chains (group g, block h): table lookups, 2 T MFMAs, scaling
+  // by the block constant, in a pipeline: the lookups of chain c + 1 go out,
+  // then chain c - 1 is scaled, then the MFMAs of chain c start, so that
+  // neither the LDS nor the MFMA latency is waited for on its own.
   auto compute = [&](const Slot& S, int64_t d, bool tail) {
     if (!tail) d = base + 2 * d;
     const int64_t kb = 2 * d;
+    constexpr int NC = 2 * G;
+    uint32_t cw[G][4];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       u32x4 c;
@@ -137,23 +149,42 @@ void k_qrows(RowsArgs p) {
       for (int j = 0; j < 2; ++j) c[j] = __builtin_amdgcn_mov_dpp(c[j], 0xE4, 0xf, 0xf, false);
       const auto s02 = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
       const auto s13 = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
-      const uint32_t cw[4] = {s02[0], s13[0], s02[1], s13[1]};
+      cw[g][0] = s02[0];
+      cw[g][1] = s13[0];
+      cw[g][2] = s02[1];
+      cw[g][3] = s13[1];
+    }
+    u32x4 wl[2][2];
+    float ch[2];
+    f32x4 s[T];
+    auto lookup = [&](int c) {
+      const int g = c >> 1, h = c & 1;
+      wl[c & 1][0] = levels8(cw[g][2 * h], lut + i16);
+      wl[c & 1][1] = levels8(cw[g][2 * h + 1], lut + i16);
+      ch[c & 1] = (h && tail) ? 0.0f : crow_t[g][kb + h];
+    };
+    lookup(0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bf16x8 w0 = as_bf16x8(levels8(cw[2 * h], lut + i16));
-        const bf16x8 w1 = as_bf16x8(levels8(cw[2 * h + 1], lut + i16));
-        const float ch = (h && tail) ? 0.0f : crow_t[g][kb + h];
-        f32x4 s[T];
+    for (int c = 0; c <= NC; ++c) {
+      const float prev = ch[(c + 1) & 1];  // of chain c - 1, before lookup(c + 1) takes its place
+      if (c + 1 < NC) lookup(c + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (c > 0) {
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[(c - 1) >> 1][t][v] += prev * s[t][v];
+      }
+      if (c < NC) {
+        const int h = c & 1;
+        const bf16x8 w0 = as_bf16x8(wl[c & 1][0]), w1 = as_bf16x8(wl[c & 1][1]);
 #pragma unroll
         for (int t = 0; t < T; ++t)
           s[t] = mfma16(as_bf16x8(S.x[t][2 * h]), w0, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int t = 0; t < T; ++t) s[t] = mfma16(as_bf16x8(S.x[t][2 * h + 1]), w1, s[t]);
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[g][t][v] += ch * s[t][v];
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -191,7 +222,7 @@ void k_qrows(RowsArgs p) {
       const int c = c0 + tid;
       const int o = (int)(n0 * kblocks) + 16 * c;
       const u32x4 qv = __builtin_amdgcn_raw_buffer_load_b128(qrs, c < nchunk ? o : INT32_MIN, 0, 0);
-      const float st = p.step[c < nchunk && o >> 8 < glast ? o >> 8 : glast];
+      const float st = p.step[c < nchunk && o >> 8 < glast ? o >> 8 : glast] * (1.0f / level_factor<CT>());
       if (c0 == 0 && tid < uquads) sum_u(tid);
       if (c < nchunk) {
         int row = 16 * c / kbl, kb = 16 * c - row * kbl;
@@ -208,18 +239,18 @@ void k_qrows(RowsArgs p) {
       const int row = e / kbl, kb = e - row * kbl;
       const int64_t n = n0 + row < N ? n0 + row : N - 1;
       const int64_t ci = n * cblocks + (kb >> p.bshift);
-      chat[row * kbs + kb] = (float)p.q8[ci] * p.step[ci >> 8];
+      chat[row * kbs + kb] = (float)p.q8[ci] * (p.step[ci >> 8] * (1.0f / level_factor<CT>()));
     }
     if (tid < uquads) sum_u(tid);
   }
   for (int e = tid + NT; e < uquads; e += NT) sum_u(e);
   {
     static_assert(kLutWords == 8 * NT, "table split");
-    const float lo = level_of<CT>(p.ut, (tid >> 4) & 15);
+    const float lo = level_of<CT>(p.ut, (tid >> 4) & 15) * level_factor<CT>();
     const int hi0 = __builtin_amdgcn_readfirstlane(tid >> 8);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      lut[tid + NT * i] = pack_bf16x2(lo, level_of<CT>(p.ut, hi0 + 2 * i));
+      lut[tid + NT * i] = pack_bf16x2(lo, level_of<CT>(p.ut, hi0 + 2 * i) * level_factor<CT>());
   }
   __syncthreads();
 
@@ -338,9 +369,9 @@ hipError_t launch(const RowsArgs& a, int code, hipStream_t stream) {
 // Whether this kernel is the faster one, from the shapes alone: the rounds of
 // workgroups over 256 compute units times a workgroup's time, here and in the
 // tiles (128 x 128 while the 256 x 256 ones would leave half the chip idle).
-// Measured with 24 adapters of rank 16, all kernels of the call, here / tiles:
-// 61 rows over 8192 x 8192 TODO us, 512 over 4096 x 4096 TODO, 64 and 96 over
-// 28672 x 8192 TODO.
+// Measured with 24 adapters of rank 16, us a call, here / tiles: 64 rows over
+// 8192 x 8192 40 / 142, 256 rows 103 / 145, 512 rows 187 / 159; 512 over 4096 x
+// 4096 68 / 97; 64 over 28672 x 8192 112 / 145, 128 rows 176 / 150.
 bool qrows_takes(int64_t M, int64_t N, int64_t K, int32_t r) {
   const int T = M <= 32 ? 2 : 4;
   if (M > kQRowsMaxM || 4 * rows_lds_words(2, T, (r + 7) / 8 * 8, K / 64) > 160 * 1024) return false;
@@ -356,7 +387,14 @@ hipError_t launch_qrows(const Nf4View& w, const uint16_t* xfrag, int64_t M, cons
                         const int32_t* index, uint16_t* Y, hipStream_t stream) {
   const RowsArgs a{w.codes, w.q8, w.step, xfrag, M, w.N, w.K, part, slices, (r + 7) / 8 * 8, B, r,
                    index, adapters, Y, w.bshift, w.ut};
-  return M <= 32 ? launch<2, 2>(a, w.code, stream) : launch<2, 4>(a, w.code, stream);
+  if (M > 32) return launch<2, 4>(a, w.code, stream);
+  // Up to 32 tokens: 64 weight rows per workgroup halve the X traffic where
+  // that leaves every compute unit its workgroup's worth of rows (17 tokens over
+  // 11008 x 4096: 29.7 -> 24.6 us a call, over 28672 x 8192: 75.7 -> 59.5; over
+  // 8192 x 8192, 128 workgroups, 28.1 -> 34.5).
+  const bool wide = (w.N + 31) / 32 > 256 &&
+                    4 * rows_lds_words(4, 2, a.ldp, w.K / 64) <= 160 * 1024;
+  return wide ? launch<4, 2>(a, w.code, stream) : launch<2, 2>(a, w.code, stream);
 }
 
 }  // namespace qn

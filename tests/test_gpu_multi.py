@@ -156,9 +156,9 @@ def test_one_adapter_is_the_layer(M):
     assert float((Y.double() - Z.double()).norm() / Z.double().norm()) <= U
     none = qn.qlora_linear_multi_fwd(w, X, A, B, s, spread(M, 4, "none"))
     base = qn.qlora_linear_fwd(w, X, torch.zeros_like(A[0]), torch.zeros_like(B[0]), 1.0)
-    # without an adapter both are X W^T: the same kernels but for batches whose
-    # weight enters as level times constant here alone
-    if M == 17:
+    # without an adapter both are X W^T: the same tiles for many rows, else the
+    # weight enters as level times constant, with levels rounded in other places
+    if M <= 17:
         assert float((none.double() - base.double()).norm() / base.double().norm()) <= U
     else:
         assert torch.equal(none, base)
