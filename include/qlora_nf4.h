@@ -341,7 +341,8 @@ int32_t qlora_linear_fwd_noalloc(const nf4_tensor_t* w, const uint16_t* X,
  * blog section "Where the memory goes"):
  *   Y_i = X_i W^T + s_a (X_i A_a^T) B_a^T,   a = index[i]
  * and Y_i = X_i W^T where index[i] lies outside 0 .. n_adapters - 1.
- *   w, X, M, Y   as in qlora_linear_fwd, M at most 2^26
+ *   w, X, M, Y   as in qlora_linear_fwd, M at most 2^26; Y overlaps no input (at
+ *                X's address: QLORA_ERR_INVALID)
  *   A, B         [n_adapters, r, K] and [n_adapters, N, r] bf16, contiguous
  *                (adapters of smaller rank padded with zeros), n_adapters >= 1,
  *                1 <= r <= 256; any size together

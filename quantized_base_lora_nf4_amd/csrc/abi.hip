@@ -490,7 +490,7 @@ int32_t qlora_linear_multi_fwd(const nf4_tensor_t* w, const uint16_t* X, int64_t
   const int32_t chk = check_fwd(w, X, M, A, B, r, 1.0f, Y, nullptr);
   if (chk != QLORA_OK) return chk;
   if (M > kMultiMaxRows || n_adapters < 1 || !s || ((uintptr_t)s & 3u) != 0 || !index ||
-      ((uintptr_t)index & 3u) != 0 || !ws || !aligned16(ws))
+      ((uintptr_t)index & 3u) != 0 || !ws || !aligned16(ws) || Y == X)
     return QLORA_ERR_INVALID;
   const int64_t N = w->N, K = w->K;
   if (ws_bytes < qlora_multi_workspace_size(M, N, K, r)) return QLORA_ERR_WORKSPACE;

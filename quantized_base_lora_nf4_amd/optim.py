@@ -186,12 +186,14 @@ def adamw_values(state: AdamWState, stream=None):
 
 
 class AdamW(torch.optim.Optimizer):
-    """AdamW with states in 32 or 8 bits, one kernel pass per parameter group.
+    """AdamW with states in 32 or 8 bits, one kernel pass per parameter group,
+    for parameters on one GPU.
 
     max_norm: the gradients of all groups are clipped by their global norm
     within the step (step() leaves them as they are; the norm before clipping
     is in `last_norm`).  masters: bfloat16 parameters are updated through
-    float32 masters kept here, and take their rounded values."""
+    float32 masters kept here, and take their rounded values; after parameters
+    were changed in another way (a checkpoint loaded), call take_masters()."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, bits: int = 32, max_norm: Optional[float] = None,
@@ -216,6 +218,18 @@ class AdamW(torch.optim.Optimizer):
         masters = [p.detach().float() if p.dtype == torch.bfloat16 else None for p in ps] \
             if self.use_masters else None
         self._kept.append({"state": adamw_init(ps, self.bits), "masters": masters, "step": 0})
+
+    @torch.no_grad()
+    def take_masters(self) -> None:
+        """Set the masters to the parameters' present values."""
+        for group, kept in zip(self.param_groups, self._kept):
+            for p, m in zip(group["params"], kept["masters"] or ()):
+                if m is not None:
+                    m.copy_(p)
+
+    def __getstate__(self):   # of copies and pickles
+        own = {n: getattr(self, n) for n in ("bits", "max_norm", "use_masters", "last_norm", "_kept")}
+        return {**super().__getstate__(), **own}
 
     @torch.no_grad()
     def step(self, closure=None):

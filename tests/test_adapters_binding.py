@@ -172,7 +172,7 @@ def test_abi_adamw_values(args):
 def _multi(w=None, **kw):
     t = dict(codes=P, q8=P, step=P, N=64, K=128, blocksize=64, dq_blocksize=256, code_type=0, levels=None)
     t.update(w or {})
-    a = dict(X=P, M=40, A=P, B=P, s=P, n=3, r=8, index=P, Y=P, ws=P, ws_bytes=1 << 30)
+    a = dict(X=P, M=40, A=P, B=P, s=P, n=3, r=8, index=P, Y=2 * P, ws=P, ws_bytes=1 << 30)
     a.update(kw)
     return _lib.lib().qlora_linear_multi_fwd(ctypes.byref(Nf4Tensor(*t.values())), *a.values(), None)
 
@@ -185,7 +185,7 @@ def _multi(w=None, **kw):
     (dict(r=257), INVALID), (dict(ws_bytes=100), WORKSPACE), (dict(M=3, ws_bytes=100), WORKSPACE),
     (dict(M=5000, ws_bytes=100), WORKSPACE), (dict(w=dict(N=60)), INVALID), (dict(w=dict(K=96)), INVALID),
     (dict(w=dict(blocksize=32)), UNSUPPORTED), (dict(w=dict(code_type=9)), UNSUPPORTED),
-    (dict(w=dict(code_type=4)), INVALID),
+    (dict(w=dict(code_type=4)), INVALID), (dict(Y=P), INVALID),
 ])
 def test_abi_multi(kw, status):
     assert _multi(**kw) == status

@@ -430,6 +430,40 @@ def test_masters_keep_small_updates():
     assert (b == 1).all() and torch.allclose(a.float(), torch.full((64,), 1 - 64 * 2.0 ** -12, device="cuda"), atol=2.0 ** -8)
 
 
+def test_masters_follow_loaded_parameters():
+    a = [torch.nn.Parameter(torch.ones(300, dtype=BF, device="cuda"))]
+    opt = qn.AdamW(a, lr=0.0, weight_decay=0.0, masters=True)
+    with torch.no_grad():
+        a[0].fill_(5.0)
+    opt.take_masters()
+    a[0].grad = torch.ones_like(a[0])
+    opt.step()
+    assert (a[0] == 5).all()
+
+
+def test_optimizer_copies():
+    import copy
+    a = _module()
+    x = qn.AdamW(a, lr=1e-2, bits=8, masters=True)
+    _train(a, x, 2)
+    b, y = copy.deepcopy((a, x))
+    assert y.param_groups[0]["params"][0] is b[0]
+    _train(a, x, 2, seed=3)
+    _train(b, y, 2, seed=3)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_optimizer_with_a_schedule():
+    a = _module()
+    opt = qn.AdamW(a, lr=1.0, weight_decay=0.0)
+    sched = torch.optim.lr_scheduler.LambdaLR(opt, lambda i: 0.0 if i else 1.0)
+    _train(a, opt, 1)
+    sched.step()
+    before = [p.detach().clone() for p in a]
+    _train(a, opt, 1)
+    assert all(torch.equal(p, q) for p, q in zip(a, before))
+
+
 def test_optimizer_groups_and_missing_gradients():
     a = _module()
     opt = qn.AdamW([{"params": a[:1], "lr": 0.0}, {"params": a[1:], "lr": 0.1}], weight_decay=0.0, bits=8)
