@@ -7,11 +7,12 @@
 // split K, codes are expanded to unscaled bf16 levels by a byte-indexed table
 // in LDS, and the block constant multiplies each 64-element block's fp32 sum.
 // Here up to 16 T tokens share the expanded codes: T MFMA column tiles per
-// code word.  Every workgroup reads all of X (from L2; G = 2 halves that
+// code word.  Every workgroup reads all of X (from L2; G = 4 halves that
 // traffic), so it comes in the order of the MFMA operands, 1 KB per load, as
 // the down products write it: read in rows, whose fragments put neighbouring
-// lanes 2 K bytes apart, 64 rows over 8192 x 8192 took 47 instead of 29 us.  More tokens make
-// more workgroups (grid dimension y), which find the weight in the caches.
+// lanes 2 K bytes apart, 64 rows over 8192 x 8192 took 47 instead of 29 us.
+// More tokens make more workgroups (grid dimension y), which find the weight in
+// the caches.
 //
 // The LoRA term is added in the epilogue from U = X A^T (multi.hip), summed
 // over its slices and scaled into LDS at the start; every output reads the
@@ -19,11 +20,12 @@
 //
 // Operand layout and double steps: see gemv.hip.
 //
-// Measured, 64 rows over 8192 x 8192: 27 us (the weight alone: 7 us at a large
-// copy's rate), of which about 8 before and after the loop.  The loop is bound
-// by X: 256 workgroups read 1 MB each, 16 TB/s out of the L2s.  With X and codes
-// from one place (all hits) it takes 9 us instead of 18; without the table
-// lookups, or with the chains of a step one after the other, the same 18.
+// Measured, 64 rows over 8192 x 8192, rank 32: 24 us (the weight alone: 7 us at
+// a large copy's rate), about 8 of them before and after the loop.  128 rows
+// with G = 4: 35 us, where G = 2 takes two rounds of workgroups, 46 us.  In the
+// loop a compute unit's parts come close to each other: per step of 128 columns
+// and 8 waves (G = 4, T = 4) 0.5 us of MFMAs, about 1 us each of vector
+// instructions, of table lookups and of X through the L1; it takes 3.
 #include "kernels.hpp"
 
 namespace qn {
@@ -56,22 +58,27 @@ struct RowsArgs {
   UserTable ut;
 };
 
-// LDS in words: byte table, U of the workgroup's tokens, their adapters, then
-// the block constants during the main loop and the waves' sums after it.
+// LDS in words: U of the workgroup's tokens, their adapters, then the byte table
+// and the block constants during the main loop, the waves' sums after it.
 __host__ __device__ constexpr int64_t rows_lds_words(int G, int T, int64_t ldp, int64_t kblocks) {
   const int64_t chat = 16 * G * (kblocks | 1), red = (int64_t)KW * G * T * 256;
-  return kLutWords + 16 * T * ldp + 16 * T + (chat > red ? chat : red);
+  return 16 * T * ldp + 16 * T + (kLutWords + chat > red ? kLutWords + chat : red);
 }
 
 template <int G, int T, class CT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2)))
 void k_qrows(RowsArgs p) {
   extern __shared__ __attribute__((aligned(16))) float lds[];
-  uint32_t* lut = reinterpret_cast<uint32_t*>(lds);
-  float* ush = lds + kLutWords;                                // [16 T][ldp]
+  // Steps of loads in flight: a step's registers are loaded anew as soon as they
+  // have been used.  A second set for the larger tiles spills outside the loop,
+  // or costs time without (64 rows over 8192 x 8192: 41.3 against 37.3 us a call;
+  // 17 over 28672 x 8192, G = 4: 63.5 against 61.6).
+  constexpr int kAhead = G * T > 4 ? 1 : 2;
+  float* ush = lds;                                            // [16 T][ldp]
   int* own = reinterpret_cast<int*>(ush + 16 * T * p.ldp);     // [16 T]
-  float* chat = reinterpret_cast<float*>(own + 16 * T);        // [16 G][kblocks | 1]
-  float* red = chat;                                           // [KW][G][T][4][64]
+  uint32_t* lut = reinterpret_cast<uint32_t*>(own + 16 * T);
+  float* chat = reinterpret_cast<float*>(lut + kLutWords);     // [16 G][kblocks | 1]
+  float* red = reinterpret_cast<float*>(lut);                                           // [KW][G][T][4][64]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, q = lane >> 4;
@@ -110,33 +117,38 @@ void k_qrows(RowsArgs p) {
     HalfRaw<CT::kBits> c[G];
     u32x4 x[T][4];
   };
-  auto issue = [&](Slot& S, int64_t d, bool tail) {
-    if (d >= d1 && !tail) d = d1 - 1;
-    if (!tail) d = base + 2 * d;
-    const int64_t kb = 2 * d;
+  // The parts of a step's loads: the codes, and X of its block h.
+  auto issue_codes = [&](Slot& S, int64_t d, bool tail) {
+    const int64_t kb = 2 * (tail ? d : base + 2 * d);
     const int64_t off = ((tail && q >= 2) ? kb - 1 : kb) * block_bytes<CT>();
-    const int64_t kb2 = tail ? kb : kb + 1;
 #pragma unroll
     for (int g = 0; g < G; ++g) S.c[g] = load_half<CT>(crow[g] + off);
+  };
+  auto issue_x = [&](Slot& S, int64_t d, int h, bool tail) {
+    const int64_t kb = 2 * (tail ? d : base + 2 * d) + (tail ? 0 : h);
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        S.x[t][j] = *reinterpret_cast<const u32x4*>(
-            xt[t] + (2 * ((j >> 1) ? kb2 : kb) + (j & 1)) * 512 + lane * 8);
+      for (int j = 0; j < 2; ++j)
+        S.x[t][2 * h + j] = *reinterpret_cast<const u32x4*>(xt[t] + (2 * kb + j) * 512 + lane * 8);
+  };
+  auto issue = [&](Slot& S, int64_t d, bool tail) {
+    issue_codes(S, d, tail);
+    issue_x(S, d, 0, tail);
+    issue_x(S, d, 1, tail);
   };
   f32x4 acc[G][T];
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[g][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // One step as 2 G chains (group g, block h): table lookups, 2 T MFMAs, scaling
+  // One step as 2 G chains (block h, group g): table lookups, 2 T MFMAs, scaling
   // by the block constant, in a pipeline: the lookups of chain c + 1 go out,
   // then chain c - 1 is scaled, then the MFMAs of chain c start, so that
-  // neither the LDS nor the MFMA latency is waited for on its own.
-  auto compute = [&](const Slot& S, int64_t d, bool tail) {
-    if (!tail) d = base + 2 * d;
-    const int64_t kb = 2 * d;
+  // neither the LDS nor the MFMA latency is waited for on its own.  The loads
+  // of step d + kAhead (if `refill`) go out as soon as their registers are free.
+  auto compute = [&](Slot& S, int64_t d, bool tail, bool refill) {
+    const int64_t kb = 2 * (tail ? d : base + 2 * d);
     constexpr int NC = 2 * G;
     uint32_t cw[G][4];
 #pragma unroll
@@ -154,11 +166,13 @@ void k_qrows(RowsArgs p) {
       cw[g][2] = s02[1];
       cw[g][3] = s13[1];
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (refill) issue_codes(S, d + kAhead, false);
     u32x4 wl[2][2];
     float ch[2];
     f32x4 s[T];
     auto lookup = [&](int c) {
-      const int g = c >> 1, h = c & 1;
+      const int h = c / G, g = c % G;
       wl[c & 1][0] = levels8(cw[g][2 * h], lut + i16);
       wl[c & 1][1] = levels8(cw[g][2 * h + 1], lut + i16);
       ch[c & 1] = (h && tail) ? 0.0f : crow_t[g][kb + h];
@@ -173,22 +187,24 @@ void k_qrows(RowsArgs p) {
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[(c - 1) >> 1][t][v] += prev * s[t][v];
+          for (int v = 0; v < 4; ++v) acc[(c - 1) % G][t][v] += prev * s[t][v];
       }
       if (c < NC) {
-        const int h = c & 1;
+        const int h = c / G;
         const bf16x8 w0 = as_bf16x8(wl[c & 1][0]), w1 = as_bf16x8(wl[c & 1][1]);
 #pragma unroll
         for (int t = 0; t < T; ++t)
           s[t] = mfma16(as_bf16x8(S.x[t][2 * h]), w0, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int t = 0; t < T; ++t) s[t] = mfma16(as_bf16x8(S.x[t][2 * h + 1]), w1, s[t]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (refill && c % G == G - 1) issue_x(S, d + kAhead, h, false);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  Slot sl[2];
+  Slot sl[kAhead];
   if (d1 > 0) issue(sl[0], 0, false);
 
   // Prologue: the tokens' adapters and U (rows without an adapter read what is
@@ -254,23 +270,28 @@ void k_qrows(RowsArgs p) {
   }
   __syncthreads();
 
-  // one step of loads in flight (codes three steps ahead: 48 registers spilled
-  // at T = 4, and nothing gained at T = 2)
   int64_t d = 0;
-  for (; d + 2 <= d1; d += 2) {
-    issue(sl[1], d + 1, false);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(sl[0], d, false);
-    __builtin_amdgcn_sched_barrier(0);
-    issue(sl[0], d + 2, false);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(sl[1], d + 1, false);
-    __builtin_amdgcn_sched_barrier(0);
+  if constexpr (kAhead == 2) {
+    if (d1 > 1) issue(sl[1], 1, false);
+    for (; d + 4 <= d1; d += 2) {
+      compute(sl[0], d, false, true);
+      compute(sl[1], d + 1, false, true);
+    }
+    if (d + 3 <= d1) {
+      compute(sl[0], d, false, true);
+      compute(sl[1], d + 1, false, false);
+      compute(sl[0], d + 2, false, false);
+    } else {
+      if (d < d1) compute(sl[0], d, false, false);
+      if (d + 1 < d1) compute(sl[1], d + 1, false, false);
+    }
+  } else {
+    for (; d + 1 < d1; ++d) compute(sl[0], d, false, true);
+    if (d < d1) compute(sl[0], d, false, false);
   }
-  if (d < d1) compute(sl[0], d, false);
   if (odd_tail) {
-    issue(sl[1], D, true);
-    compute(sl[1], D, true);
+    issue(sl[0], D, true);
+    compute(sl[0], D, true, false);
   }
   // Outputs o = tid + NT k of [g][t][v][lane].  The first adapter columns are
   // on their way while the waves' sums go through LDS.
@@ -366,20 +387,49 @@ hipError_t launch(const RowsArgs& a, int code, hipStream_t stream) {
 
 }  // namespace
 
-// Whether this kernel is the faster one, from the shapes alone: the rounds of
-// workgroups over 256 compute units times a workgroup's time, here and in the
-// tiles (128 x 128 while the 256 x 256 ones would leave half the chip idle).
-// Measured with 24 adapters of rank 16, us a call, here / tiles: 64 rows over
-// 8192 x 8192 40 / 142, 256 rows 103 / 145, 512 rows 187 / 159; 512 over 4096 x
-// 4096 68 / 97; 64 over 28672 x 8192 112 / 145, 128 rows 176 / 150.
-bool qrows_takes(int64_t M, int64_t N, int64_t K, int32_t r) {
+namespace {
+
+struct Shape {
+  int G, T;
+  double us;  // estimate; 0 if no tile fits
+};
+
+int64_t over(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The tile and its time, from the shapes alone: the rounds of workgroups over
+// 256 compute units times a workgroup's time.  Measured with 24 adapters of
+// rank 32, us a call, G = 2 / G = 4: 64 rows over 8192 x 8192 37 / 47, 128 rows
+// 58 / 48, 256 rows 100 / 79; 64 over 11008 x 4096 40 / 34; 64 over 28672 x 8192
+// 106 / 83.  Up to 32 rows: 17 over 11008 x 4096 29.7 / 24.6, over 28672 x 8192
+// 75.7 / 61.6, over 8192 x 8192, where G = 4 leaves half the chip idle, 28 / 35.
+Shape shape_of(int64_t M, int64_t N, int64_t K, int32_t r) {
   const int T = M <= 32 ? 2 : 4;
-  if (M > kQRowsMaxM || 4 * rows_lds_words(2, T, (r + 7) / 8 * 8, K / 64) > 160 * 1024) return false;
-  const auto over = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const int64_t here = over(N, 32) * over(M, 16 * T);
+  const auto fits = [&](int G) {
+    return 4 * rows_lds_words(G, T, (r + 7) / 8 * 8, K / 64) <= 160 * 1024;
+  };
+  const auto rounds = [&](int G) { return (double)over(over(N, 16 * G) * over(M, 16 * T), 256); };
+  if (!fits(2)) return {2, T, 0.0};
+  const double two = rounds(2) * (6.0 + (T == 2 ? 0.0015 : 0.0021) * K);
+  const double four = rounds(4) * (T == 2 ? 6.0 + 0.0023 * K : 5.0 + 0.0036 * K);
+  return fits(4) && four < two ? Shape{4, T, four} : Shape{2, T, two};
+}
+
+}  // namespace
+
+// Whether this kernel is the faster one, against an estimate of the tiles (128 x
+// 128 while the 256 x 256 ones would leave half the chip idle): a round of
+// workgroups, the weight's stream, the rows' order.  Measured as above, here /
+// tiles: 256 rows over 8192 x 8192 79 / 151, 512 rows 143 / 144, 1024 rows 268 /
+// 217; 384 over 11008 x 4096 121 / 125, 512 rows 144 / 126; 128 over 28672 x 8192
+// 145 / 171, 256 rows 242 / 226; 512 over 4096 x 4096 60 / 88.
+bool qrows_takes(int64_t M, int64_t N, int64_t K, int32_t r) {
+  if (M > kQRowsMaxM) return false;
+  const Shape here = shape_of(M, N, K, r);
   const int64_t big = over(M, 256) * over(N, 256), small = over(M, 128) * over(N, 128);
-  const double tile = over(2 * big <= 256 ? small : big, 256) * (K / 64 * 1.1 + 10.0);
-  return over(here, 256) * (6.0 + 0.0023 * K) < tile;
+  const double unit = K / 64 * 0.9 + 5.0;
+  const double tiles = 2 * big <= 256 ? unit * (0.55 + 0.45 * (double)over(small, 256))
+                                      : 1.9 * unit * (double)over(big, 256);
+  return here.us > 0.0 && here.us < tiles + (double)N * K * 1e-7 + 8.0;
 }
 
 hipError_t launch_qrows(const Nf4View& w, const uint16_t* xfrag, int64_t M, const float* part,
@@ -387,14 +437,9 @@ hipError_t launch_qrows(const Nf4View& w, const uint16_t* xfrag, int64_t M, cons
                         const int32_t* index, uint16_t* Y, hipStream_t stream) {
   const RowsArgs a{w.codes, w.q8, w.step, xfrag, M, w.N, w.K, part, slices, (r + 7) / 8 * 8, B, r,
                    index, adapters, Y, w.bshift, w.ut};
-  if (M > 32) return launch<2, 4>(a, w.code, stream);
-  // Up to 32 tokens: 64 weight rows per workgroup halve the X traffic where
-  // that leaves every compute unit its workgroup's worth of rows (17 tokens over
-  // 11008 x 4096: 29.7 -> 24.6 us a call, over 28672 x 8192: 75.7 -> 59.5; over
-  // 8192 x 8192, 128 workgroups, 28.1 -> 34.5).
-  const bool wide = (w.N + 31) / 32 > 256 &&
-                    4 * rows_lds_words(4, 2, a.ldp, w.K / 64) <= 160 * 1024;
-  return wide ? launch<4, 2>(a, w.code, stream) : launch<2, 2>(a, w.code, stream);
+  const Shape s = shape_of(M, w.N, w.K, r);
+  if (s.T == 4) return s.G == 4 ? launch<4, 4>(a, w.code, stream) : launch<2, 4>(a, w.code, stream);
+  return s.G == 4 ? launch<4, 2>(a, w.code, stream) : launch<2, 2>(a, w.code, stream);
 }
 
 }  // namespace qn

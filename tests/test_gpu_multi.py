@@ -108,6 +108,17 @@ def test_sizes(M, N, K):
     check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
+@pytest.mark.parametrize("M", [20, 70])
+@pytest.mark.parametrize("r,K", [(8, 64), (33, 576), (64, 1024), (100, 192), (128, 448)])
+@pytest.mark.parametrize("code", ["nf4", "nf3", "nf2"])
+def test_wide_weights(M, r, K, code):
+    """So many weight rows that workgroups take 64 of them, the last ones fewer."""
+    say(f"[multi] {M} rows, 16392 x {K}, rank {r}, {code}")
+    w, A, B, s = make(16392, K, 5, r, code)
+    X, index = rows(M, K), spread(M, 5, "random")
+    check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
+
+
 @pytest.mark.parametrize("M", [4, 30, 100, 4100])
 @pytest.mark.parametrize("code,blocksize", [("nf4", 128), ("nf4", 256), ("fp4", 64), ("nf3", 64), ("nf2", 128), ("user4", 64)])
 def test_code_types(M, code, blocksize):
