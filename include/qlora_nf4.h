@@ -692,7 +692,8 @@ int32_t qlora_grad_norm(int64_t n, const void* const* grads, const int64_t* size
  *                kernels in place of lr and step (a captured step replays with
  *                their values at that time), or NULL
  *   norm         one float (device), the gradients' norm; NULL: no clipping
- *   max_norm     >= 0 (not NaN), with norm
+ *   max_norm     >= 0 (not NaN), with norm; the factor min(1, max_norm / (norm +
+ *                1e-6)) is rounded once, from fp64
  * The host arrays are read during the call and not kept.
  * 8-bit states: codes with a scale s per block, the block's largest |m| and v,
  *   m = s c |c| / 127^2,  c in -127..127;   v = s (c / 255)^4,  c in 0..255.
@@ -720,7 +721,8 @@ typedef struct qlora_adamw_t {
   const float* lr_dev;
   const int64_t* step_dev;
   const float* norm;
-  float eps, max_norm;
+  float eps;
+  double max_norm;
   int32_t state_bits;
 } qlora_adamw_t;
 /* Blocks of states of n tensors; -1 for invalid sizes (2^31 blocks or more). */

@@ -169,7 +169,7 @@ class AdamW(ctypes.Structure):
         ("step_dev", ctypes.c_void_p),
         ("norm", ctypes.c_void_p),
         ("eps", ctypes.c_float),
-        ("max_norm", ctypes.c_float),
+        ("max_norm", ctypes.c_double),
         ("state_bits", ctypes.c_int32),
     ]
 

@@ -384,7 +384,7 @@ int32_t qlora_adamw_step(const qlora_adamw_t* a, hipStream_t stream) {
   const auto rate_ok = [](double x) { return x >= 0.0 && isfinite(x); };
   if ((a->step < 1 && !a->step_dev) || !rate_ok(a->lr) || !beta_ok(a->beta1) ||
       !beta_ok(a->beta2) || !rate_ok(a->weight_decay) || !rate_ok(a->eps) ||
-      (a->norm && !(a->max_norm >= 0.0f)))
+      (a->norm && !(a->max_norm >= 0.0)))
     return QLORA_ERR_INVALID;
   if (!aligned(a->lr_dev, 4) || !aligned(a->step_dev, 8) || !aligned(a->norm, 4))
     return QLORA_ERR_INVALID;

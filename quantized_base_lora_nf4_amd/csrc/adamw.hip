@@ -186,8 +186,8 @@ __device__ __forceinline__ Step step_of(const AdamHyper& h) {
   s.rb2 = (float)(1.0 / sqrt(bc2));
   s.c = 1.0f;
   if (h.norm) {  // as in clipping: NaN passes through, an infinite norm gives 0
-    const double f = (double)h.max_norm / ((double)*h.norm + 1e-6);
-    const bool free = h.max_norm == __builtin_inff() && *h.norm == __builtin_inff();
+    const double f = h.max_norm / ((double)*h.norm + 1e-6);
+    const bool free = h.max_norm == __builtin_inf() && *h.norm == __builtin_inff();
     s.c = f >= 1.0 || free ? 1.0f : (float)f;
   }
   return s;

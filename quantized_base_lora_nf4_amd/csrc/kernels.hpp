@@ -222,7 +222,8 @@ struct AdamHyper {
   const float* lr_dev;           // device scalars, or null
   const int64_t* step_dev;
   const float* norm;             // the gradients' norm, or null: no clipping
-  float max_norm, eps;
+  double max_norm;
+  float eps;
 };
 struct AdamArgs {
   int64_t n;

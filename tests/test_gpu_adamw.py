@@ -187,11 +187,22 @@ def test_copies(bits):
                                            (float("inf"), float("inf"))])
 def test_clipping(bits, norm, max_norm):
     c = Case([1000, 64], [F32], [BF], bits)
-    factor = float(np.float32(oracle.clip_factor(np.float32(norm), np.float32(max_norm))))
+    factor = float(np.float32(oracle.clip_factor(np.float32(norm), max_norm)))
     t = torch.tensor([norm], device="cuda")
     before = [g.clone() for g in c.grads]
     c.check(5, factor=factor, run=step(c, 5, norm=t, max_norm=max_norm))
     assert all(torch.equal(a, b) for a, b in zip(before, c.grads))
+
+
+def test_clipping_factor_is_rounded_once():
+    """From the limit as it is given: its own rounding to fp32 would move the
+    factor by a step for about half of the norms."""
+    p, g = torch.zeros(1, device="cuda"), torch.ones(1, device="cuda")
+    rng = np.random.default_rng(7)
+    for n in rng.uniform(1.0, 20.0, 64).astype(np.float32):
+        st, limit = qn.adamw_init([p], bits=32), float(n) * 0.7
+        qn.adamw_step([p], [g], st, 1, 0.0, betas=(0.0, 0.0), norm=torch.tensor([n], device="cuda"), max_norm=limit)
+        assert float(st.m[0]) == np.float32(oracle.clip_factor(n, limit))
 
 
 def test_clipping_with_grad_norm_is_clip_then_step():
