@@ -16,12 +16,12 @@
 // the same bits wherever they are computed; square roots only guess a code,
 // which a comparison with the threshold then settles.
 //
-// One pass over the data, bound by HBM (bf16 parameters and gradients: 22
-// bytes per element with 32-bit states, 10 with 8-bit ones, where about 75
-// instructions per element come close to the same time).  32 lanes own a
-// block, 8 elements each, so the block's largest values are a reduction
-// within half a wave.  The tensors' addresses travel in the launch arguments,
-// as in clip.hip.
+// One pass over the data.  32 lanes own a block, 8 elements each, so the block's
+// largest values are a reduction within half a wave.  The tensors' addresses
+// travel in the launch arguments, as in clip.hip.  Measured, 160 M bf16
+// parameters in 448 tensors: 32-bit states (22 bytes per element) 722 us, 4.9
+// TB/s, bound by HBM; 8-bit states (10 bytes) 420 us, 3.8 TB/s, where about 75 issue
+// slots per element take as long as the memory.
 #include "kernels.hpp"
 
 namespace qn {
@@ -127,19 +127,20 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
 // ... and the factor that maps it to the largest code's power.
 __device__ __forceinline__ float factor_of(float s, float top) { return s > 0.0f ? top / s : 0.0f; }
 
-// The code of a value whose power is y (at most one rounding above the largest
-// code's; a NaN counts as 0): the guess from a root that is within a few units
-// in the last place is the code or one less.
+// The code of a value whose power is y (at most a few roundings above the largest
+// code's): the guess from a root that is within a few units in the last place,
+// taken a little low, is the code or one less.
 __device__ __forceinline__ float code_m(float y) {
 #pragma clang fp contract(off)
   const float n = floorf(__builtin_amdgcn_sqrtf(y) + 0.4999f);
   const float h = n + 0.5f;
   return h * h <= y ? h + 0.5f : n;
 }
-// root: the square root of y, within a few units (0 for y below 2^-96: code 0 or 1).
-__device__ __forceinline__ float code_v(float y, float root) {
+// low: the square root of y, less 2^-20 of it, within a few units (0 for y below
+// 2^-96: code 0 or 1).  Its root is 127 2^-20 below the code's at most.
+__device__ __forceinline__ float code_v(float y, float low) {
 #pragma clang fp contract(off)
-  const float n = floorf(__builtin_amdgcn_sqrtf(root) + 0.4999f);
+  const float n = rintf(__builtin_amdgcn_sqrtf(low));
   const float h = n + 0.5f, h2 = h * h;  // exact
   return h2 * h2 <= y ? h + 0.5f : n;
 }
@@ -270,7 +271,7 @@ __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, ui
       }
       if constexpr (k8) {
         const uint32_t a = __builtin_bit_cast(uint32_t, m[j][i]) & 0x7fffffffu;
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[j][i]) & 0x7fffffffu;
+        const uint32_t b = __builtin_bit_cast(uint32_t, v[j][i]);  // no negative ones
         mtop = mtop > a ? mtop : a;
         vtop = vtop > b ? vtop : b;
       }
@@ -296,7 +297,9 @@ __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, ui
     ms = scale_of(half_max(mtop));
     vs = scale_of(half_max(vtop));
     const float fm = factor_of(ms, 16129.0f), fv = factor_of(vs, 4228250625.0f);
-    const float rv = __builtin_amdgcn_sqrtf(fv), least = fv > 0.0f ? 1.0f : 0.0f;
+    // (a block without scales, also one that holds a NaN, gets codes 0)
+    const float rv = __builtin_amdgcn_sqrtf(fv) * (1.0f - 0x1p-20f);
+    const uint32_t keep_m = fm > 0.0f ? ~0u : 0u, keep_v = fv > 0.0f ? ~0u : 0u;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = j * 32 * W + lane * W;
@@ -306,16 +309,14 @@ __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, ui
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = m[j][4 * q + i], y = v[j][4 * q + i];
-          // A factor of 0, also that of a NaN scale, gives code 0: the median
-          // with a NaN is the lowest of the others.
-          const float a = code_m(__builtin_amdgcn_fmed3f(fabsf(x) * fm, 0.0f, 65536.0f));
-          const float c = code_v(__builtin_amdgcn_fmed3f(y * fv, 0.0f, 0x1p+36f), root[j][4 * q + i] * rv);
-          const float b = __builtin_amdgcn_fmed3f(c, y > 0.0f ? least : 0.0f, 255.0f);
+          const float a = code_m(fabsf(x) * fm);
+          const float c = code_v(y * fv, root[j][4 * q + i] * rv);
+          const float b = y > 0.0f ? fmaxf(c, 1.0f) : c;
           wm = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_copysignf(a, x) + 128.0f, i, wm);
           wv = __builtin_amdgcn_cvt_pk_u8_f32(b, i, wv);
         }
-        cm[j].w[q] = wm ^ 0x80808080u;
-        cv[j].w[q] = wv;
+        cm[j].w[q] = (wm ^ 0x80808080u) & keep_m;
+        cv[j].w[q] = wv & keep_v;
       }
       *reinterpret_cast<Codes<W>*>((uint8_t*)st.m + blk * kBlock + e) = cm[j];
       *reinterpret_cast<Codes<W>*>((uint8_t*)st.v + blk * kBlock + e) = cv[j];
@@ -328,8 +329,9 @@ __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, ui
 }
 
 // The chunks k0 .. k1 - 1 of one tensor, of `blocks` blocks, the last of which
-// has `tail` elements.  The next chunk's loads are in flight under the
-// arithmetic of this one.
+// has `tail` elements.  With 32-bit states the next chunk's loads are in flight
+// under the arithmetic of this one (755 -> 722 us for 160 M bf16 elements); with
+// 8-bit ones the registers cost more than that (327 us against 302 for 115 M).
 template <bool k8, class PT, class GT>
 __device__ __forceinline__ void update_chunks(PT* p, const GT* g, uint16_t* c, const State& st,
                                               int64_t first, int64_t k0, int64_t k1, int64_t blocks,
@@ -337,14 +339,17 @@ __device__ __forceinline__ void update_chunks(PT* p, const GT* g, uint16_t* c, c
   const auto size_of = [&](int64_t b) { return b == blocks - 1 ? tail : kBlock; };
   int64_t b = k0 * kChunk + (threadIdx.x >> 5);  // this half wave's block of each chunk
   const int64_t end = k1 * kChunk < blocks ? k1 * kChunk : blocks;
-  Raw<k8, PT, GT> a, n;
-  if (b < end) a.load_block(p + b * kBlock, g + b * kBlock, st, first + b, size_of(b));
-  while (b < end) {
-    const int64_t nb = b + kChunk;
-    if (nb < end) n.load_block(p + nb * kBlock, g + nb * kBlock, st, first + nb, size_of(nb));
+  Raw<k8, PT, GT> a;
+  const auto load_at = [&](Raw<k8, PT, GT>& x, int64_t i) {
+    if (i < end) x.load_block(p + i * kBlock, g + i * kBlock, st, first + i, size_of(i));
+  };
+  if constexpr (!k8) load_at(a, b);
+  for (; b < end; b += kChunk) {
+    Raw<k8, PT, GT> n;
+    if constexpr (k8) load_at(a, b);
+    else load_at(n, b + kChunk);
     update_block<k8>(a, p + b * kBlock, c ? c + b * kBlock : nullptr, st, first + b, size_of(b), s);
-    a = n;
-    b = nb;
+    if constexpr (!k8) a = n;
   }
 }
 
