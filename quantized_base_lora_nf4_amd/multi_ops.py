@@ -37,9 +37,10 @@ def qlora_linear_multi_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: to
             raise ValueError(f"{name} must be {nd}-D")
     M, N, K = X.shape[0], w.N, w.K
     n, r = A.shape[:2]
-    # (the types of the weight's tensors are checked above)
-    for name, t in (("codes", w.codes), ("q8", w.q8), ("step", w.step)):
-        _same(name, t, t.shape, (t.dtype,), dev)
+    # (the weight's types are checked above, its layout with its struct below)
+    for name, t in (("q8", w.q8), ("step", w.step)):
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
     _same("X", X, (M, K), _SIXTEEN, dev)
     _same("A", A, (n, r, K), _SIXTEEN, dev)
     _same("B", B, (n, N, r), _SIXTEEN, dev)

@@ -182,6 +182,19 @@ def test_copies(bits):
     c.check(2, copies=copies, run=step(c, 2, copies=copies))
 
 
+def test_copies_of_all():
+    """Every parameter with a copy, and each way in which one of them does not fit."""
+    c = Case([300, 64, 7], [F32], [F32], 32)
+    copies = [torch.zeros_like(p, dtype=BF) for p in c.params]
+    c.check(2, copies=copies, run=step(c, 2, copies=copies))
+    before = [p.clone() for p in c.params]
+    for bad, error in ((copies[1].float(), TypeError), (copies[1].cpu(), ValueError), (copies[1].view(8, 8), ValueError),
+                       (torch.zeros(64, 2, dtype=BF, device="cuda")[:, 0], ValueError), (3, TypeError)):
+        with pytest.raises(error):
+            step(c, 3, copies=[copies[0], bad, copies[2]])()
+    assert all(torch.equal(a, b) for a, b in zip(before, c.params))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("norm,max_norm", [(2.0, 0.3), (0.1, 0.3), (2.0, 0.0), (1e-20, 1e-20), (float("inf"), 1.0),
                                            (float("inf"), float("inf"))])
