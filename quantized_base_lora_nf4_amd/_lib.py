@@ -180,6 +180,22 @@ class QloraError(RuntimeError):
         super().__init__(f"{what}: status {status} ({status_str(status)})")
 
 
+_tensors = None
+
+
+def tensors():
+    """The compiled reader of lists of tensors (csrc/tensors.cpp)."""
+    global _tensors
+    if _tensors is None:
+        try:
+            from . import _tensors as found
+        except ImportError as e:
+            raise RuntimeError("the reader of tensor lists is not built. Run `python -m "
+                               "quantized_base_lora_nf4_amd.build` (hipcc, gfx950).") from e
+        _tensors = found
+    return _tensors
+
+
 _lib = None
 
 

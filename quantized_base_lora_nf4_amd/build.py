@@ -4,13 +4,15 @@
 
 Each csrc/*.hip file is compiled by hipcc into _build/ and the objects are
 linked into quantized_base_lora_nf4_amd/libqlora_nf4.so.  Packed-fp32 VALU
-instructions are disabled for every device compile.
+instructions are disabled for every device compile.  csrc/tensors.cpp, host code
+of the binding that reads torch's tensors, becomes _tensors.so beside it.
 """
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
+TENSORS = os.path.join(PKG, "_tensors.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -47,11 +50,28 @@ def _compile(src):
     return obj
 
 
+def _compile_tensors():
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = TENSORS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-I{sysconfig.get_paths()['include']}", *(f"-isystem{p}" for p in include_paths()),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           os.path.join(CSRC, "tensors.cpp"), "-o", tmp, *(f"-L{p}" for p in library_paths()),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        host = ex.submit(_compile_tensors)
         objs = list(ex.map(_compile, srcs))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,97 @@
+// What the Python binding reads of every tensor in a list, in one call: at
+// hundreds of tensors per optimizer step the attributes, read one by one from
+// Python, take longer than the step's kernels.  Whatever is not the ordinary
+// case is left to the Python code, which names what is wrong.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <algorithm>
+#include <vector>
+
+#include <torch/csrc/autograd/python_variable.h>
+
+namespace {
+
+// describe(tensors, ptrs, sizes, types, bf16, f32) -> int
+//
+// tensors: a list; ptrs, sizes, types: addresses of as many uint64, int64 and
+// int32, which take each tensor's address, number of elements and type (the
+// numbers bf16 and f32).  Returns the index of the GPU that all are on; -1 if
+// one of them is not a contiguous bfloat16 or float32 tensor of the first one's
+// GPU.
+PyObject* describe(PyObject*, PyObject* args) {
+  PyObject* list;
+  unsigned long long ptrs, sizes, types;
+  int bf16, f32;
+  if (!PyArg_ParseTuple(args, "O!KKKii", &PyList_Type, &list, &ptrs, &sizes, &types, &bf16, &f32))
+    return nullptr;
+  long device = -1;
+  try {
+    const Py_ssize_t n = PyList_GET_SIZE(list);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject* const o = PyList_GET_ITEM(list, i);
+      if (!THPVariable_Check(o)) return PyLong_FromLong(-1);
+      const at::Tensor& t = THPVariable_Unpack(o);
+      const c10::ScalarType ty = t.scalar_type();
+      if (!t.is_cuda() || t.layout() != c10::kStrided ||
+          (ty != c10::ScalarType::BFloat16 && ty != c10::ScalarType::Float) || !t.is_contiguous())
+        return PyLong_FromLong(-1);
+      if (i == 0) device = t.get_device();
+      if (t.get_device() != device) return PyLong_FromLong(-1);
+      reinterpret_cast<uint64_t*>(ptrs)[i] = reinterpret_cast<uint64_t>(t.data_ptr());
+      reinterpret_cast<int64_t*>(sizes)[i] = t.numel();
+      reinterpret_cast<int32_t*>(types)[i] = ty == c10::ScalarType::Float ? f32 : bf16;
+    }
+  } catch (...) {
+    return PyLong_FromLong(-1);
+  }
+  return PyLong_FromLong(device);
+}
+
+// same_shapes(a, b) -> bool: two lists of tensors, as many with the same shapes.
+PyObject* same_shapes(PyObject*, PyObject* args) {
+  PyObject *a, *b;
+  if (!PyArg_ParseTuple(args, "O!O!", &PyList_Type, &a, &PyList_Type, &b)) return nullptr;
+  try {
+    const Py_ssize_t n = PyList_GET_SIZE(a);
+    if (PyList_GET_SIZE(b) != n) Py_RETURN_FALSE;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject *const x = PyList_GET_ITEM(a, i), *const y = PyList_GET_ITEM(b, i);
+      if (!THPVariable_Check(x) || !THPVariable_Check(y) ||
+          THPVariable_Unpack(x).sizes() != THPVariable_Unpack(y).sizes())
+        Py_RETURN_FALSE;
+    }
+  } catch (...) {
+    Py_RETURN_FALSE;
+  }
+  Py_RETURN_TRUE;
+}
+
+// distinct(ptrs, n) -> bool: n addresses, no two alike.
+PyObject* distinct(PyObject*, PyObject* args) {
+  unsigned long long ptrs;
+  Py_ssize_t n;
+  if (!PyArg_ParseTuple(args, "Kn", &ptrs, &n)) return nullptr;
+  const uint64_t* const p = reinterpret_cast<const uint64_t*>(ptrs);
+  Py_ssize_t i = 1;
+  while (i < n && p[i - 1] < p[i]) ++i;
+  if (i >= n) Py_RETURN_TRUE;  // in order already
+  try {
+    std::vector<uint64_t> s(p, p + n);
+    std::sort(s.begin(), s.end());
+    if (std::adjacent_find(s.begin(), s.end()) == s.end()) Py_RETURN_TRUE;
+  } catch (...) {
+  }
+  Py_RETURN_FALSE;
+}
+
+PyMethodDef methods[] = {{"describe", describe, METH_VARARGS, nullptr},
+                         {"same_shapes", same_shapes, METH_VARARGS, nullptr},
+                         {"distinct", distinct, METH_VARARGS, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensors() { return PyModule_Create(&module); }

@@ -5,17 +5,14 @@ the tensors' device unless a stream is passed."""
 
 import array
 import math
-import operator
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from ._lib import QLORA_ADAMW_BLOCK, check, lib
+from ._lib import QLORA_ADAMW_BLOCK, QLORA_TYPE_BF16, check, lib, tensors
 from ._lib import AdamW as _Args
-from .train_ops import _device_of, _dtype_of, _grad_arrays, _on, _ptr_of, _same, grad_norm
-
-_shape_of = operator.attrgetter("shape")
+from .train_ops import _describe, _device_of, _grad_arrays, _on, _ptr_of, _same, grad_norm
 
 
 @dataclass
@@ -90,18 +87,6 @@ def _scalar(name, x, dtype, device):
     return 0, x.data_ptr()
 
 
-def _all_like(copies, params, device) -> bool:
-    """Whether all copies are contiguous bfloat16 tensors of their parameters'
-    shapes (False also if one is None)."""
-    try:
-        return (set(map(_dtype_of, copies)) == {torch.bfloat16} and
-                set(map(torch.Tensor.get_device, copies)) == {device.index} and
-                all(map(torch.Tensor.is_contiguous, copies)) and
-                list(map(_shape_of, copies)) == list(map(_shape_of, params)))
-    except (AttributeError, TypeError):
-        return False
-
-
 def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay: float = 0.01, norm: Optional[torch.Tensor] = None,
                max_norm: Optional[float] = None, copies=None, stream=None) -> None:
@@ -128,17 +113,20 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
     if len(grads) != n:
         raise ValueError(f"{len(grads)} gradients for {n} parameters")
     dev, ptrs, sizes, types = _grad_arrays("params", params)
-    if len(set(ptrs)) != n:
+    if not tensors().distinct(_ptr_of(ptrs), n):
         given = [p.data_ptr() for p in params if p.numel()]
         if len(set(given)) != len(given):
             raise ValueError("a parameter is given twice")
-    there = [g for g in grads if g is not None]
-    if not there:
-        return
-    gdev, gptrs, gsizes, gtypes = _grad_arrays("grads", there)
+    got = _describe(grads)
+    if got is None:  # some are None, or not what they should be
+        there = [g for g in grads if g is not None]
+        if not there:
+            return
+        got = _grad_arrays("grads", there)
+    gdev, gptrs, gsizes, gtypes = got
     if gdev != dev:
         raise ValueError(f"grads are on {gdev}, expected {dev}")
-    if len(there) != n:
+    if len(gptrs) != n:
         at = [i for i, g in enumerate(grads) if g is not None]
         if [sizes[i] for i in at] != gsizes.tolist():
             raise ValueError("a gradient has another size than its parameter")
@@ -154,11 +142,15 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
         copies = list(copies)
         if len(copies) != n:
             raise ValueError(f"{len(copies)} copies for {n} parameters")
-        if not _all_like(copies, params, dev):
+        got = _describe(copies)
+        if (got is not None and got[0] == dev and got[3].count(QLORA_TYPE_BF16) == n and
+                tensors().same_shapes(copies, params)):
+            cptrs = got[1]
+        else:
             for p, c in zip(params, copies):
                 if c is not None:
                     _same("copy", c, p.shape, (torch.bfloat16,), dev)
-        cptrs = array.array("Q", [0 if c is None else c.data_ptr() for c in copies])
+            cptrs = array.array("Q", [0 if c is None else c.data_ptr() for c in copies])
     if (norm is None) != (max_norm is None):
         raise ValueError("norm and max_norm go together")
     if norm is not None:

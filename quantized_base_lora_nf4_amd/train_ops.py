@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Rope, check, lib
+from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Rope, check, lib, tensors
 from .ops import _stream_obj
 
 _SIXTEEN = (torch.bfloat16, torch.int16, torch.uint16)
@@ -594,8 +594,23 @@ class RMSNorm(torch.nn.Module):
 _dtype_of = operator.attrgetter("dtype")
 
 
-def _grad_arrays(name: str, grads):
+def _describe(tensors_list: list):
+    """(device, addresses, sizes, types) of a list of contiguous bfloat16 and
+    float32 tensors on one GPU; None if one of them is not that, or not a
+    tensor."""
+    n = len(tensors_list)
+    ptrs, sizes, types = (array.array(c, bytes(w * n)) for c, w in (("Q", 8), ("q", 8), ("i", 4)))
+    at = tensors().describe(tensors_list, _ptr_of(ptrs), _ptr_of(sizes), _ptr_of(types),
+                            _TYPES[torch.bfloat16], _TYPES[torch.float32])
+    return None if at < 0 else (tensors_list[0].device, ptrs, sizes, types)
+
+
+def _grad_arrays(name: str, grads: list):
     """(device, addresses, sizes, types) of a list of gradients."""
+    got = _describe(grads)
+    if got is not None:
+        return got
+    # what is wrong with them
     if not isinstance(grads[0], torch.Tensor):
         raise TypeError(f"{name} must all be torch tensors")
     dev = _device_of(f"{name}[0]", grads[0])

@@ -227,3 +227,26 @@ def test_step_barriers_of_the_many_adapter_tiles():
             assert waits.tile_covered(seg), f"{name}: a step barrier may run before the tile landed"
             checked += 1
     assert checked >= 4 * 14
+
+
+def test_tensor_lists():
+    """The compiled reader: ordinary lists only (its values are tested on the GPU)."""
+    import array
+    from quantized_base_lora_nf4_amd._lib import tensors
+    T = tensors()
+    x = [torch.zeros(3, 2), torch.zeros(3, 2)]
+    room = array.array("Q", bytes(64))
+    at = room.buffer_info()[0]
+    for bad in (x, [3], [None], [], [x[0], "a"], [torch.zeros(2, device="meta")]):
+        assert T.describe(bad, at, at, at, 0, 1) == -1
+    assert not any(room)
+    for args in (((1, 2), at, at, at, 0, 1), (x, at), (x, "a", at, at, 0, 1)):
+        with pytest.raises(TypeError):
+            T.describe(*args)
+    assert T.same_shapes(x, [torch.ones(3, 2, dtype=torch.int8)] * 2) and T.same_shapes([], [])
+    for other in ([x[0]], [x[0], torch.zeros(2, 3)], [x[0], torch.zeros(6)], [x[0], None]):
+        assert not T.same_shapes(x, other)
+    for values, apart in (([], True), ([5], True), ([1, 2, 9], True), ([9, 1, 2], True), ([3, 3], False),
+                          ([7, 1, 8, 1], False), ([2**64 - 1, 0, 2**63], True)):
+        a = array.array("Q", values)
+        assert T.distinct(a.buffer_info()[0], len(a)) is apart

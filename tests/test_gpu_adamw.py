@@ -536,3 +536,18 @@ def test_refusals(make, error, match):
     with pytest.raises(error, match=match):
         make(p, g, qn.adamw_init(p))
     assert not p[0].any() and not p[1].any()
+
+
+def test_tensor_lists():
+    """The compiled reader of lists of tensors: what torch says of each, and
+    None for whatever is not a contiguous tensor of the two types."""
+    from quantized_base_lora_nf4_amd.train_ops import _TYPES, _describe
+    base = torch.zeros(1000, device="cuda")
+    ok = [base, base[3:9], base.view(10, 100)[2:4], torch.nn.Parameter(torch.zeros(5, 7, dtype=BF, device="cuda")),
+          torch.zeros(0, 4, device="cuda"), base[7], base.view(1000, 1)[::2][:1], torch.zeros(3, 4, dtype=BF, device="cuda")[1:]]
+    dev, ptrs, sizes, types = _describe(ok)
+    assert dev == base.device and ptrs.tolist() == [t.data_ptr() for t in ok]
+    assert sizes.tolist() == [t.numel() for t in ok] and types.tolist() == [_TYPES[t.dtype] for t in ok]
+    for bad in (base[::2], base.view(10, 100).t(), base.half(), base.double(), base.cpu(), None, 3, base.to_sparse(),
+                torch.zeros(2, device="meta")):
+        assert _describe([base, bad]) is None and _describe([bad, base]) is None
