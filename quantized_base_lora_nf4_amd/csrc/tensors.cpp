@@ -67,6 +67,58 @@ PyObject* same_shapes(PyObject*, PyObject* args) {
   Py_RETURN_TRUE;
 }
 
+bool type_fits(char kind, c10::ScalarType t) {
+  switch (kind) {
+    case 's':
+      return t == c10::ScalarType::BFloat16 || t == c10::ScalarType::Short ||
+             t == c10::ScalarType::UInt16;
+    case 'f':
+      return t == c10::ScalarType::Float;
+    case 'i':
+      return t == c10::ScalarType::Int;
+    case 'b':
+      return t == c10::ScalarType::Byte;
+    case 'c':
+      return t == c10::ScalarType::Char;
+    default:
+      return false;
+  }
+}
+
+// fits(device, kinds, tensors, shapes) -> bool: each of the tuple `tensors` is a
+// contiguous tensor on GPU `device`, of the type that its letter in `kinds`
+// names (s: 16 bits as the layer takes them, f: float32, i: int32, b: uint8, c:
+// int8) and of the shape in the tuple `shapes`.
+PyObject* fits(PyObject*, PyObject* args) {
+  long device;
+  const char* kinds;
+  Py_ssize_t n;
+  PyObject *list, *shapes;
+  if (!PyArg_ParseTuple(args, "ls#O!O!", &device, &kinds, &n, &PyTuple_Type, &list, &PyTuple_Type,
+                        &shapes))
+    return nullptr;
+  if (PyTuple_GET_SIZE(list) != n || PyTuple_GET_SIZE(shapes) != n) Py_RETURN_FALSE;
+  try {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject *const o = PyTuple_GET_ITEM(list, i), *const shape = PyTuple_GET_ITEM(shapes, i);
+      if (!THPVariable_Check(o) || !PyTuple_Check(shape)) Py_RETURN_FALSE;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!t.is_cuda() || t.layout() != c10::kStrided || t.get_device() != device ||
+          !type_fits(kinds[i], t.scalar_type()) || !t.is_contiguous() ||
+          t.dim() != PyTuple_GET_SIZE(shape))
+        Py_RETURN_FALSE;
+      for (int64_t d = 0; d < t.dim(); ++d) {
+        const long long want = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, d));
+        if (want == -1 && PyErr_Occurred()) return nullptr;
+        if (t.size(d) != want) Py_RETURN_FALSE;
+      }
+    }
+  } catch (...) {
+    Py_RETURN_FALSE;
+  }
+  Py_RETURN_TRUE;
+}
+
 // distinct(ptrs, n) -> bool: n addresses, no two alike.
 PyObject* distinct(PyObject*, PyObject* args) {
   unsigned long long ptrs;
@@ -87,6 +139,7 @@ PyObject* distinct(PyObject*, PyObject* args) {
 
 PyMethodDef methods[] = {{"describe", describe, METH_VARARGS, nullptr},
                          {"same_shapes", same_shapes, METH_VARARGS, nullptr},
+                         {"fits", fits, METH_VARARGS, nullptr},
                          {"distinct", distinct, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,

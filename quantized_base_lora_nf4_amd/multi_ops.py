@@ -8,7 +8,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import check, lib
+from ._lib import check, lib, tensors
 from .ops import NF4Weight, QLoRALinear, _check_weight
 from .train_ops import _SIXTEEN, _bytes, _on, _same, _scratch
 
@@ -35,17 +35,19 @@ def qlora_linear_multi_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: to
             raise TypeError(f"{name} must be a torch tensor")
         if t.dim() != nd:
             raise ValueError(f"{name} must be {nd}-D")
-    M, N, K = X.shape[0], w.N, w.K
-    n, r = A.shape[:2]
+    M, N, K = len(X), w.N, w.K
+    n, r, _ = A.shape
     # (the weight's types are checked above, its layout with its struct below)
     for name, t in (("q8", w.q8), ("step", w.step)):
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    _same("X", X, (M, K), _SIXTEEN, dev)
-    _same("A", A, (n, r, K), _SIXTEEN, dev)
-    _same("B", B, (n, N, r), _SIXTEEN, dev)
-    _same("s", s, (n,), (torch.float32,), dev)
-    _same("index", index, (M,), (torch.int32,), dev)
+    if not tensors().fits(dev.index, "sssfi", (X, A, B, s, index),
+                          ((M, K), (n, r, K), (n, N, r), (n,), (M,))):
+        _same("X", X, (M, K), _SIXTEEN, dev)
+        _same("A", A, (n, r, K), _SIXTEEN, dev)
+        _same("B", B, (n, N, r), _SIXTEEN, dev)
+        _same("s", s, (n,), (torch.float32,), dev)
+        _same("index", index, (M,), (torch.int32,), dev)
     if Y is not None:
         _same("Y", Y, (M, N), _SIXTEEN, dev)
     st, ctx = _on(dev, stream)

@@ -64,6 +64,15 @@ def _check_state(state: AdamWState, device) -> int:
     if not isinstance(state, AdamWState):
         raise TypeError("state must be an AdamWState")
     m, v, ms, vs = state.m, state.v, state.m_scale, state.v_scale
+    if isinstance(m, torch.Tensor):
+        n = m.numel()
+        blocks = n // QLORA_ADAMW_BLOCK
+        if n % QLORA_ADAMW_BLOCK == 0 and (
+                tensors().fits(device.index, "cbff", (m, v, ms, vs), ((n,), (n,), (blocks,), (blocks,)))
+                if ms is not None else
+                vs is None and tensors().fits(device.index, "ff", (m, v), ((n,), (n,)))):
+            return blocks
+    # what is wrong with it
     if not isinstance(m, torch.Tensor) or m.dim() != 1 or m.numel() % QLORA_ADAMW_BLOCK:
         raise ValueError(f"state.m must be a 1-D tensor of a multiple of {QLORA_ADAMW_BLOCK} elements")
     eight = m.dtype == torch.int8

@@ -243,6 +243,9 @@ def test_tensor_lists():
     for args in (((1, 2), at, at, at, 0, 1), (x, at), (x, "a", at, at, 0, 1)):
         with pytest.raises(TypeError):
             T.describe(*args)
+    for bad in ((0, "f", (x[0],), ((3, 2),)), (0, "f", (3,), ((3,),)), (0, "ff", (x[0],), ((3, 2),)), (0, "f", (x[0],), (None,))):
+        assert not T.fits(*bad)
+    assert T.fits(0, "", (), ())
     assert T.same_shapes(x, [torch.ones(3, 2, dtype=torch.int8)] * 2) and T.same_shapes([], [])
     for other in ([x[0]], [x[0], torch.zeros(2, 3)], [x[0], torch.zeros(6)], [x[0], None]):
         assert not T.same_shapes(x, other)

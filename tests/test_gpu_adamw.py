@@ -551,3 +551,18 @@ def test_tensor_lists():
     for bad in (base[::2], base.view(10, 100).t(), base.half(), base.double(), base.cpu(), None, 3, base.to_sparse(),
                 torch.zeros(2, device="meta")):
         assert _describe([base, bad]) is None and _describe([bad, base]) is None
+    from quantized_base_lora_nf4_amd._lib import tensors
+    fits, kinds = tensors().fits, {"s": [BF, torch.int16, torch.uint16], "f": [F32], "i": [torch.int32], "b": [torch.uint8],
+                                   "c": [torch.int8]}
+    x = torch.zeros(4, 6, device="cuda")
+    every = [t for ts in kinds.values() for t in ts] + [torch.int64, torch.float64, torch.bool, torch.float16]
+    for kind, types in kinds.items():
+        for t in every:
+            assert fits(0, kind, (x.to(t),), ((4, 6),)) == (t in types)
+    assert fits(0, "fi", (x, x.int()[0]), ((4, 6), (6,)))
+    for bad in ((1, "f", (x,), ((4, 6),)), (0, "f", (x,), ((6, 4),)), (0, "f", (x,), ((24,),)), (0, "f", (x,), ((4, 6, 1),)),
+                (0, "f", (x.t(),), ((6, 4),)), (0, "f", (x.cpu(),), ((4, 6),)), (0, "ff", (x, None), ((4, 6), (4, 6))),
+                (0, "z", (x,), ((4, 6),))):
+        assert not fits(*bad)
+    with pytest.raises(TypeError):
+        fits(0, "f", (x,), ((4, "6"),))
