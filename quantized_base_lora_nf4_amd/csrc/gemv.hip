@@ -690,14 +690,13 @@ void k_qgemv(Args p) {
     float sum[KO];
 #pragma unroll
     for (int k = 0; k < KO; ++k) sum[k] = 0.0f;
-    if ((p.r & 7) == 0) {
+    if (p.r >= 8) {
       for (int j0 = 0; j0 < p.r; j0 += JB) {
         u32x4 bq[KO][JB / 8];
 #pragma unroll
         for (int k = 0; k < KO; ++k)
 #pragma unroll
-          for (int q = 0; q < JB / 8; ++q)
-            bq[k][q] = *reinterpret_cast<const u32x4*>(bp[k] + (j0 + 8 * q < p.r ? j0 + 8 * q : 0));
+          for (int q = 0; q < JB / 8; ++q) bq[k][q] = load_row8(bp[k], j0 + 8 * q, p.r);
         __builtin_amdgcn_sched_barrier(0);  // every load of the batch before the first use
 #pragma unroll
         for (int q = 0; q < JB / 8; ++q) {
@@ -705,10 +704,12 @@ void k_qgemv(Args p) {
 #pragma unroll
           for (int k = 0; k < KO; ++k) {
             const float* ur8 = ush + (has[k] ? mk[k] * p.r : 0) + j0 + 8 * q;
+            const u32x4 b = shift_row8(bq[k][q], j0 + 8 * q, p.r);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-              const uint32_t wd = bq[k][q][t >> 1];
-              sum[k] += ur8[t] * ((t & 1) ? bf16_hi_to_f32(wd) : bf16_lo_to_f32(wd));
+              // (past r: the next token's)
+              const float u = j0 + 8 * q + t < p.r ? ur8[t] : 0.0f;
+              sum[k] += u * ((t & 1) ? bf16_hi_to_f32(b[t >> 1]) : bf16_lo_to_f32(b[t >> 1]));
             }
           }
         }

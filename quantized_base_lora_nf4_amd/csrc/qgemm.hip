@@ -512,7 +512,7 @@ __device__ __forceinline__ void multi_lora(const MultiFwdArgs& p, uint16_t* As, 
 
   const int units = (p.r + 7) >> 3, total = count * units;  // units of an adapter, of the tile
   const int64_t ldp = 8 * units;
-  const bool bvec = (p.r & 7) == 0;
+  const bool bvec = p.r >= 8;
   constexpr int NA = C::BM * 8 / C::NT, NB = C::BN * 8 / C::NT;  // 16-byte pieces per thread
   const int c8 = tid & 7;                                         // of the same unit
   for (int q0 = 0; q0 < total; q0 += 8) {
@@ -553,13 +553,13 @@ __device__ __forceinline__ void multi_lora(const MultiFwdArgs& p, uint16_t* As, 
     for (int i = 0; i < NB; ++i) {
       int64_t g = n0 + (tid >> 3) + i * (C::NT / 8);
       if (g >= p.N) g = p.N - 1;
-      const uint16_t* src = p.B + ((int64_t)list[ai] * p.N + g) * p.r + j;
+      const uint16_t* src = p.B + ((int64_t)list[ai] * p.N + g) * p.r;
       if (bvec) {
-        bv[i] = *reinterpret_cast<const u32x4*>(src);
+        bv[i] = load_row8(src, j, p.r);
       } else {
         uint16_t t[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = j + e < p.r ? src[e] : (uint16_t)0;
+        for (int e = 0; e < 8; ++e) t[e] = j + e < p.r ? src[j + e] : (uint16_t)0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) bv[i][e] = (uint32_t)t[2 * e] | ((uint32_t)t[2 * e + 1] << 16);
       }
@@ -567,7 +567,7 @@ __device__ __forceinline__ void multi_lora(const MultiFwdArgs& p, uint16_t* As, 
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int row = (tid >> 3) + i * (C::NT / 8);
-      u32x4 v = in ? bv[i] : u32x4{0u, 0u, 0u, 0u};
+      u32x4 v = in ? (bvec ? shift_row8(bv[i], j, p.r) : bv[i]) : u32x4{0u, 0u, 0u, 0u};
       // bit 15 of a half: its exponent is all ones
       u32x4 top;
 #pragma unroll

@@ -320,9 +320,9 @@ void k_qrows(RowsArgs p) {
     for (int k = 0; k < KO; ++k)
 #pragma unroll
       for (int i = 0; i < JB / 8; ++i)
-        bq[k][i] = *reinterpret_cast<const u32x4*>(bp[k] + (j0 + 8 * i < p.r ? j0 + 8 * i : 0));
+        bq[k][i] = load_row8(bp[k], j0 + 8 * i, p.r);
   };
-  const bool bvec = (p.r & 7) == 0;
+  const bool bvec = p.r >= 8;
   if (bvec) load_b(0);
   __syncthreads();  // the constants become the waves' sums
 #pragma unroll
@@ -352,9 +352,10 @@ void k_qrows(RowsArgs p) {
           const float* u = ush + mk[k] * p.ldp + j0 + 8 * i;
           const f32x4 u0 = *reinterpret_cast<const f32x4*>(u);
           const f32x4 u1 = *reinterpret_cast<const f32x4*>(u + 4);
+          const u32x4 b = shift_row8(bq[k][i], j0 + 8 * i, p.r);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint32_t w = bq[k][i][e >> 1];
+            const uint32_t w = b[e >> 1];
             lora[k] += (e < 4 ? u0[e] : u1[e - 4]) * ((e & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w));
           }
         }

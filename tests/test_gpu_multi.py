@@ -108,6 +108,21 @@ def test_sizes(M, N, K):
     check("Y", qn.qlora_linear_multi_fwd(w, X, A, B, s, index), w, X, A, B, s, index)
 
 
+@pytest.mark.parametrize("M", [5, 40, 100, 4100])
+@pytest.mark.parametrize("r", [3, 9, 13, 23, 47, 95])
+def test_rows_end_inside_a_piece(M, r):
+    """Ranks that are no multiple of 8: what follows a row of B, in the same
+    adapter or in the next, reaches no output of the row."""
+    w, A, B, s = make(136, 128, 3, r)
+    X, index = rows(M, 128), torch.zeros(M, dtype=torch.int32, device="cuda")
+    bad = B.clone()
+    bad[0, 1::2] = float("nan")
+    bad[1:] = float("inf")
+    Y, Z = (qn.qlora_linear_multi_fwd(w, X, A, b, s, index) for b in (B, bad))
+    check(f"rank {r}", Y, w, X, A, B, s, index)
+    assert torch.equal(Y[:, ::2], Z[:, ::2]) and Z[:, 1::2].isnan().all()
+
+
 @pytest.mark.parametrize("M", [20, 70])
 @pytest.mark.parametrize("r,K", [(8, 64), (33, 576), (64, 1024), (100, 192), (128, 448)])
 @pytest.mark.parametrize("code", ["nf4", "nf3", "nf2"])
