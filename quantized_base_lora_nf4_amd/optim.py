@@ -269,10 +269,11 @@ class AdamW(torch.optim.Optimizer):
             if kept["masters"] is not None:
                 copies = [None if m is None else p for p, m in zip(data, kept["masters"])]
                 data = [p if m is None else m for p, m in zip(data, kept["masters"])]
-            kept["step"] += 1
-            adamw_step(data, grads, kept["state"], kept["step"], group["lr"], group["betas"],
+            step = kept["step"] + 1
+            adamw_step(data, grads, kept["state"], step, group["lr"], group["betas"],
                        group["eps"], group["weight_decay"], norm,
                        None if norm is None else self.max_norm, copies)
+            kept["step"] = step   # (a call that refuses has updated nothing)
         return loss
 
     def state_dict(self):
