@@ -686,7 +686,9 @@ int32_t qlora_grad_norm(int64_t n, const void* const* grads, const int64_t* size
  *   m_scale, v_scale   8 bits: one float per block of QLORA_ADAMW_BLOCK elements
  *                (the last block of a tensor may be shorter); 32 bits: not used
  *   state_blocks >= qlora_adamw_blocks(n, sizes) (else QLORA_ERR_WORKSPACE)
- *   step         >= 1, the number of this step; lr, eps, weight_decay >= 0,
+ *   step         >= 1, the number of updates that the tensors have had, this one
+ *                included (tensors that have had fewer: in a call of their own,
+ *                with the others' gradients NULL); lr, eps, weight_decay >= 0,
  *                0 <= beta < 1
  *   lr_dev, step_dev   one float, one int64 on the device that are read by the
  *                kernels in place of lr and step (a captured step replays with

@@ -96,6 +96,22 @@ def _scalar(name, x, dtype, device):
     return 0, x.data_ptr()
 
 
+def _passes(steps, grads, gptrs):
+    """(step, addresses of the gradients that take part in it) of each number in
+    `steps`, one per tensor.  All are checked before the first pass."""
+    if len(steps) != len(grads):
+        raise ValueError(f"{len(steps)} steps for {len(grads)} parameters")
+    counts = {s for s, g in zip(steps, grads) if g is not None}
+    if not all(isinstance(s, int) for s in counts):
+        raise ValueError("steps must be whole numbers")
+    if min(counts) < 1:
+        raise ValueError(f"steps count from 1, one is {min(counts)}")
+    if len(counts) == 1:
+        return ((counts.pop(), gptrs),)
+    return [(c, array.array("Q", [p if s == c else 0 for p, s in zip(gptrs, steps)]))
+            for c in sorted(counts)]
+
+
 def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay: float = 0.01, norm: Optional[torch.Tensor] = None,
                max_norm: Optional[float] = None, copies=None, stream=None) -> None:
@@ -107,11 +123,13 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
 
     params: contiguous bfloat16 or float32 tensors, each given once; grads: as
     many tensors of the same sizes, of either type (None: that tensor and its
-    states are left alone); state: from adamw_init, updated.  step counts from
-    1.  norm: the one-element float32 device tensor of grad_norm, with
-    max_norm (the gradients themselves stay as they are).  copies: bfloat16
-    tensors (or None) that take the updated parameters, rounded: for parameters
-    kept in float32 beside a bfloat16 copy.
+    states are left alone); state: from adamw_init, updated.  step: the number
+    of updates that the tensors have had, this one included; a list of as many
+    numbers where they differ (tensors that had no gradient in some steps; one
+    pass for each number).  norm: the one-element float32 device tensor of
+    grad_norm, with max_norm (the gradients themselves stay as they are).
+    copies: bfloat16 tensors (or None) that take the updated parameters,
+    rounded: for parameters kept in float32 beside a bfloat16 copy.
 
     step and lr may be one-element device tensors (int64, float32), read when
     the kernels run: so a captured step can be replayed with new values."""
@@ -169,7 +187,7 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
             raise ValueError(f"norm must be a one-element float32 tensor on {dev}")
         if not max_norm >= 0.0:
             raise ValueError(f"max_norm must be at least 0, got {max_norm}")
-    step, step_dev = _scalar("step", step, torch.int64, dev)
+    passes = _passes(step, grads, gptrs) if isinstance(step, (list, tuple)) else ((step, gptrs),)
     lr, lr_dev = _scalar("lr", lr, torch.float32, dev)
     L = lib()
     if L.qlora_adamw_blocks(n, _ptr_of(sizes)) > blocks:
@@ -177,14 +195,17 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
     st, ctx = _on(dev, stream)
     eight = state.bits == 8
     with ctx:
-        check(L.qlora_adamw_step(_Args(
-            n, _ptr_of(ptrs), _ptr_of(gptrs), None if cptrs is None else _ptr_of(cptrs),
-            _ptr_of(sizes), _ptr_of(types), _ptr_of(gtypes), state.m.data_ptr(), state.v.data_ptr(),
-            state.m_scale.data_ptr() if eight else None, state.v_scale.data_ptr() if eight else None,
-            blocks, int(step), float(lr), float(betas[0]), float(betas[1]), float(weight_decay),
-            lr_dev, step_dev, None if norm is None else norm.data_ptr(), float(eps),
-            0.0 if max_norm is None else float(max_norm), 8 if eight else 32), st),
-            "qlora_adamw_step")
+        for step, gptrs in passes:
+            step, step_dev = _scalar("step", step, torch.int64, dev)
+            check(L.qlora_adamw_step(_Args(
+                n, _ptr_of(ptrs), _ptr_of(gptrs), None if cptrs is None else _ptr_of(cptrs),
+                _ptr_of(sizes), _ptr_of(types), _ptr_of(gtypes), state.m.data_ptr(),
+                state.v.data_ptr(), state.m_scale.data_ptr() if eight else None,
+                state.v_scale.data_ptr() if eight else None, blocks, int(step), float(lr),
+                float(betas[0]), float(betas[1]), float(weight_decay), lr_dev, step_dev,
+                None if norm is None else norm.data_ptr(), float(eps),
+                0.0 if max_norm is None else float(max_norm), 8 if eight else 32), st),
+                "qlora_adamw_step")
 
 
 def adamw_values(state: AdamWState, stream=None):
@@ -204,8 +225,9 @@ def adamw_values(state: AdamWState, stream=None):
 
 
 class AdamW(torch.optim.Optimizer):
-    """AdamW with states in 32 or 8 bits, one kernel pass per parameter group,
-    for parameters on one GPU.
+    """AdamW with states in 32 or 8 bits, one kernel pass per parameter group
+    (and per number of updates, which each parameter counts for itself: one
+    without a gradient is left alone), for parameters on one GPU.
 
     max_norm: the gradients of all groups are clipped by their global norm
     within the step (step() leaves them as they are; the norm before clipping
@@ -227,7 +249,7 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError(f"betas must be at least 0 and below 1, got {betas}")
         self.bits, self.max_norm, self.use_masters = bits, max_norm, masters
         self.last_norm = None
-        self._kept = []   # per group: its parameters' states, masters and step
+        self._kept = []   # per group: its parameters' states, masters and numbers of updates
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay))
 
     def add_param_group(self, group) -> None:
@@ -235,7 +257,8 @@ class AdamW(torch.optim.Optimizer):
         ps = self.param_groups[-1]["params"]
         masters = [p.detach().float() if p.dtype == torch.bfloat16 else None for p in ps] \
             if self.use_masters else None
-        self._kept.append({"state": adamw_init(ps, self.bits), "masters": masters, "step": 0})
+        self._kept.append({"state": adamw_init(ps, self.bits), "masters": masters,
+                           "step": [0] * len(ps)})
 
     @torch.no_grad()
     def take_masters(self) -> None:
@@ -249,6 +272,12 @@ class AdamW(torch.optim.Optimizer):
         own = {n: getattr(self, n) for n in ("bits", "max_norm", "use_masters", "last_norm", "_kept")}
         return {**super().__getstate__(), **own}
 
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        for k, g in zip(self._kept, self.param_groups):   # (one number per group before)
+            if isinstance(k["step"], int):
+                k["step"] = [k["step"]] * len(g["params"])
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None
@@ -256,34 +285,35 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         norm = None
+        given = [[p.grad for p in g["params"]] for g in self.param_groups]
         if self.max_norm is not None:
-            grads = [p.grad for g in self.param_groups for p in g["params"] if p.grad is not None]
-            if grads:
-                norm = self.last_norm = grad_norm(grads)
-        for group, kept in zip(self.param_groups, self._kept):
+            there = [g for grads in given for g in grads if g is not None]
+            if there:
+                norm = self.last_norm = grad_norm(there)
+        for group, kept, grads in zip(self.param_groups, self._kept, given):
             ps = group["params"]
-            grads = [p.grad for p in ps]
             if all(g is None for g in grads):
                 continue
             data, copies = [p.detach() for p in ps], None
             if kept["masters"] is not None:
                 copies = [None if m is None else p for p, m in zip(data, kept["masters"])]
                 data = [p if m is None else m for p, m in zip(data, kept["masters"])]
-            step = kept["step"] + 1
-            adamw_step(data, grads, kept["state"], step, group["lr"], group["betas"],
-                       group["eps"], group["weight_decay"], norm,
+            step = [s if g is None else s + 1 for s, g in zip(kept["step"], grads)]
+            told = {s for s, g in zip(step, grads) if g is not None}
+            adamw_step(data, grads, kept["state"], step if len(told) > 1 else told.pop(),
+                       group["lr"], group["betas"], group["eps"], group["weight_decay"], norm,
                        None if norm is None else self.max_norm, copies)
             kept["step"] = step   # (a call that refuses has updated nothing)
         return loss
 
     def state_dict(self):
-        """The groups' settings, and each group's states, masters and step
-        (tensors that later steps update: clone them to keep them)."""
+        """The groups' settings, and each group's states, masters and numbers of
+        updates (tensors that later steps update: clone them to keep them)."""
         kept = []
         for k in self._kept:
             s = k["state"]
             kept.append({"m": s.m, "v": s.v, "m_scale": s.m_scale, "v_scale": s.v_scale,
-                         "masters": k["masters"], "step": k["step"]})
+                         "masters": k["masters"], "step": list(k["step"])})
         groups = [{n: v for n, v in g.items() if n != "params"} for g in self.param_groups]
         return {"bits": self.bits, "groups": groups, "kept": kept}
 
@@ -291,7 +321,7 @@ class AdamW(torch.optim.Optimizer):
     def load_state_dict(self, d) -> None:
         if d["bits"] != self.bits or len(d["kept"]) != len(self._kept):
             raise ValueError("the states are of other bits or groups")
-        pairs = []
+        pairs, steps = [], []
         for k, new in zip(self._kept, d["kept"]):
             s = k["state"]
             here = [s.m, s.v, s.m_scale, s.v_scale, *(k["masters"] or [])]
@@ -302,8 +332,13 @@ class AdamW(torch.optim.Optimizer):
                     for a, b in zip(here, there)):
                 raise ValueError("the states are of other parameters")
             pairs += [(a, b) for a, b in zip(here, there) if a is not None]
+            # (one number for the whole group: as it was counted before)
+            count, n = new["step"], len(k["step"])
+            steps.append([int(count)] * n if isinstance(count, int) else list(map(int, count)))
+            if len(steps[-1]) != n:
+                raise ValueError("the states are of other parameters")
         for a, b in pairs:
             a.copy_(b)
-        for k, g, new, settings in zip(self._kept, self.param_groups, d["kept"], d["groups"]):
-            k["step"] = int(new["step"])
+        for k, g, step, settings in zip(self._kept, self.param_groups, steps, d["groups"]):
+            k["step"] = step
             g.update(settings)
