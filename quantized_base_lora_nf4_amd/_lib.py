@@ -196,6 +196,12 @@ def tensors():
     return _tensors
 
 
+def written(*given) -> None:
+    """Tensors that a caller gave and a call has written into (None: not
+    given) count a new version, as after torch's operations in place."""
+    tensors().written(given)
+
+
 _lib = None
 
 

@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <algorithm>
+#include <exception>
 #include <vector>
 
 #include <torch/csrc/autograd/python_variable.h>
@@ -137,10 +138,39 @@ PyObject* distinct(PyObject*, PyObject* args) {
   Py_RETURN_FALSE;
 }
 
+// written(tensors): each tensor in a list or tuple (None entries are passed
+// over) counts a new version, as after torch's own operations in place: a
+// backward pass that saved it before raises.  Inference tensors have none.
+PyObject* written(PyObject*, PyObject* arg) {
+  PyObject* const seq = PySequence_Fast(arg, "expected a list or tuple of tensors");
+  if (!seq) return nullptr;
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+  PyObject* const* const items = PySequence_Fast_ITEMS(seq);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (items[i] == Py_None) continue;
+    if (!THPVariable_Check(items[i])) {
+      Py_DECREF(seq);
+      PyErr_SetString(PyExc_TypeError, "expected tensors");
+      return nullptr;
+    }
+    try {
+      const at::Tensor& t = THPVariable_Unpack(items[i]);
+      if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    } catch (const std::exception& e) {
+      Py_DECREF(seq);
+      PyErr_SetString(PyExc_RuntimeError, e.what());
+      return nullptr;
+    }
+  }
+  Py_DECREF(seq);
+  Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {{"describe", describe, METH_VARARGS, nullptr},
                          {"same_shapes", same_shapes, METH_VARARGS, nullptr},
                          {"fits", fits, METH_VARARGS, nullptr},
                          {"distinct", distinct, METH_VARARGS, nullptr},
+                         {"written", written, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -8,7 +8,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import check, lib, tensors
+from ._lib import check, lib, tensors, written
 from .ops import NF4Weight, QLoRALinear, _check_weight
 from .train_ops import _SIXTEEN, _bytes, _on, _same, _scratch
 
@@ -50,6 +50,7 @@ def qlora_linear_multi_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: to
         _same("index", index, (M,), (torch.int32,), dev)
     if Y is not None:
         _same("Y", Y, (M, N), _SIXTEEN, dev)
+    given = Y
     st, ctx = _on(dev, stream)
     with ctx:
         if Y is None:
@@ -60,6 +61,8 @@ def qlora_linear_multi_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: to
                                       B.data_ptr(), s.data_ptr(), n, r, index.data_ptr(), Y.data_ptr(),
                                       ws.data_ptr(), _bytes(ws), st)
     check(rc, "qlora_linear_multi_fwd")
+    if given is not None:
+        written(given)
     return Y
 
 

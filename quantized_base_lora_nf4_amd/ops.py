@@ -14,7 +14,7 @@ import torch
 
 from ._lib import (QLORA_CODE_FP4, QLORA_CODE_NF2, QLORA_CODE_NF3, QLORA_CODE_NF4,
                    QLORA_CODE_USER2, QLORA_CODE_USER3, QLORA_CODE_USER4, QLORA_ERR_INFEASIBLE,
-                   Nf4Tensor, check, lib)
+                   Nf4Tensor, check, lib, written)
 
 BLOCKSIZE = 64
 DQ_BLOCKSIZE = 256
@@ -182,6 +182,7 @@ def nf4_quantize(W: torch.Tensor, out: Optional[NF4Weight] = None, stream=None,
         st = lib().qlora_quantize(_ptr(W), N, K, cid, blocksize, DQ_BLOCKSIZE, _ptr(out.codes),
                                   _ptr(out.q8), _ptr(out.step), _stream(stream))
     check(st, "nf4_quantize")
+    written(out.codes, out.q8, out.step)
     return out
 
 
@@ -196,6 +197,7 @@ def nf4_dequantize(w: NF4Weight, out: Optional[torch.Tensor] = None, stream=None
     s = w.struct()
     check(lib().nf4_dequantize(ctypes.byref(s), _ptr(_bf16_view(out)), _stream(stream)),
           "nf4_dequantize")
+    written(out)
     return out
 
 
@@ -293,6 +295,7 @@ def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Te
                                 _ptr(Y), _ptr(U_out), _ptr(ws), ws.numel() * ws.element_size(),
                                 st.cuda_stream)
     check(rc, "qlora_linear_fwd")
+    written(Y, U_out)
     return Y
 
 
@@ -307,6 +310,7 @@ def qlora_linear_fwd_noalloc(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: 
                                         float(s), _ptr(Y), _ptr(U_out),
                                         _stream_obj(stream).cuda_stream)
     check(rc, "qlora_linear_fwd_noalloc")
+    written(Y, U_out)
     return Y
 
 
@@ -336,6 +340,7 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
                                 r, float(s), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
                                 ws.numel() * ws.element_size(), st.cuda_stream)
     check(rc, "qlora_linear_bwd")
+    written(dX, dA, dB)
     return dX, dA, dB
 
 
@@ -404,6 +409,7 @@ def quant_error(W: torch.Tensor, code: str = "nf4", L1: Optional[torch.Tensor] =
                                   r, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                   _stream(stream))
     check(st, "qlora_config_error")
+    written(out)
     return out
 
 

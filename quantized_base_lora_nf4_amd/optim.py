@@ -10,7 +10,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import QLORA_ADAMW_BLOCK, QLORA_TYPE_BF16, check, lib, tensors
+from ._lib import QLORA_ADAMW_BLOCK, QLORA_TYPE_BF16, check, lib, tensors, written
 from ._lib import AdamW as _Args
 from .train_ops import _describe, _device_of, _grad_arrays, _on, _ptr_of, _same, grad_norm
 
@@ -153,6 +153,7 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
     gdev, gptrs, gsizes, gtypes = got
     if gdev != dev:
         raise ValueError(f"grads are on {gdev}, expected {dev}")
+    some = None
     if len(gptrs) != n:
         at = [i for i, g in enumerate(grads) if g is not None]
         if [sizes[i] for i in at] != gsizes.tolist():
@@ -206,6 +207,11 @@ def adamw_step(params, grads, state: AdamWState, step, lr, betas=(0.9, 0.999), e
                 None if norm is None else norm.data_ptr(), float(eps),
                 0.0 if max_norm is None else float(max_norm), 8 if eight else 32), st),
                 "qlora_adamw_step")
+    for given in (params, copies):
+        if given is not None:
+            tensors().written(given if some is None else
+                              [t for t, g in zip(given, grads) if g is not None])
+    written(state.m, state.v, state.m_scale, state.v_scale)
 
 
 def adamw_values(state: AdamWState, stream=None):

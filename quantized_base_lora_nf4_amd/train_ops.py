@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Rope, check, lib, tensors
+from ._lib import QLORA_TYPE_BF16, QLORA_TYPE_FP32, Attention, Rope, check, lib, tensors, written
 from .ops import _stream_obj
 
 _SIXTEEN = (torch.bfloat16, torch.int16, torch.uint16)
@@ -195,6 +195,7 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
     c = _AttnCall(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     st, ctx = _on(c.dev, stream)
     with ctx:
+        given = out
         if out is None:
             out = c.new(q, False)
         else:
@@ -206,6 +207,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
         check(L.qlora_attention_fwd(c.c, *c.views(), lse.data_ptr(),
                                     None if ws is None else ws.data_ptr(), _bytes(ws), st),
               "qlora_attention_fwd")
+    if given is not None:
+        written(given)
     return out, lse
 
 
@@ -236,6 +239,8 @@ def attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Te
         w = c.views()
         check(L.qlora_attention_bwd(c.c, *w[:4], lse.data_ptr(), *w[4:], ws.data_ptr(),
                                     _bytes(ws), st), "qlora_attention_bwd")
+    if out is not None:
+        written(dq, dk, dv)
     return dq, dk, dv
 
 
@@ -390,6 +395,8 @@ def _rope_call(names, q, k, inv_freq, positions, cu_seqlens, interleaved, scale,
         check(lib().qlora_rope(Rope(nseq, rows, cu, pos, psb, pst, inv_freq.data_ptr(), pbytes, heads,
                                     kv, dim, rot, int(interleaved), inverse, float(scale)),
                                base, base + 32, base + 64, base + 96, st), "qlora_rope")
+    if out is not None:
+        written(qo, ko if kv else None)
     return qo, ko
 
 
@@ -483,6 +490,7 @@ def norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     dev, rows, width = _check_norm(x, weight)
     if bias is not None:
         _same("bias", bias, weight.shape, (weight.dtype,), dev)
+    given = out
     if out is not None:
         _same("out", out, x.shape, (x.dtype,), dev)
     st, ctx = _on(dev, stream)
@@ -497,6 +505,8 @@ def norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
                                    _TYPES[weight.dtype], float(eps), int(rms), out.data_ptr(),
                                    None if rms else mean.data_ptr(), rstd.data_ptr(), st),
               "qlora_norm_fwd")
+    if given is not None:
+        written(given)
     return out, mean, rstd
 
 
@@ -675,6 +685,10 @@ def _clip_call(grads, max_norm, out, ws, stream):
                                          max_norm, None if outs is None else _ptr_of(outs),
                                          norm_out.data_ptr(), ws.data_ptr(), _bytes(ws), st),
                   "qlora_clip_grad_norm")
+            if isinstance(out, torch.Tensor):
+                written(out)
+            else:
+                tensors().written(grads if out is None else out)
     return norm_out
 
 
