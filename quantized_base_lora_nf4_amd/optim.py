@@ -314,22 +314,30 @@ class AdamW(torch.optim.Optimizer):
 
     def state_dict(self):
         """The groups' settings, and each group's states, masters and numbers of
-        updates (tensors that later steps update: clone them to keep them)."""
+        updates (tensors that later steps update: clone them to keep them), with
+        the shapes of its parameters."""
         kept = []
-        for k in self._kept:
+        for k, g in zip(self._kept, self.param_groups):
             s = k["state"]
             kept.append({"m": s.m, "v": s.v, "m_scale": s.m_scale, "v_scale": s.v_scale,
-                         "masters": k["masters"], "step": list(k["step"])})
+                         "masters": k["masters"], "step": list(k["step"]),
+                         "shapes": [tuple(p.shape) for p in g["params"]]})
         groups = [{n: v for n, v in g.items() if n != "params"} for g in self.param_groups]
         return {"bits": self.bits, "groups": groups, "kept": kept}
 
     @torch.no_grad()
     def load_state_dict(self, d) -> None:
-        if d["bits"] != self.bits or len(d["kept"]) != len(self._kept):
+        """States of the same parameters in the same order and groups."""
+        if (d["bits"] != self.bits or len(d["kept"]) != len(self._kept) or
+                len(d["groups"]) != len(self.param_groups)):
             raise ValueError("the states are of other bits or groups")
         pairs, steps = [], []
-        for k, new in zip(self._kept, d["kept"]):
+        for k, g, new in zip(self._kept, self.param_groups, d["kept"]):
             s = k["state"]
+            # (states of 256-element blocks alone do not tell whose they are)
+            shapes = [tuple(p.shape) for p in g["params"]]
+            if [tuple(x) for x in new.get("shapes", shapes)] != shapes:
+                raise ValueError("the states are of other parameters")
             here = [s.m, s.v, s.m_scale, s.v_scale, *(k["masters"] or [])]
             there = [new["m"], new["v"], new["m_scale"], new["v_scale"], *(new["masters"] or [])]
             if len(here) != len(there) or any(

@@ -88,3 +88,50 @@ def test_copies_keep_the_counts(monkeypatch):
     assert _counts(opt) == [0, 0, 2] and _counts(other) == [0, 0, 1]
     opt._kept[0]["step"] = 5   # a copy of the time when the group had one count
     assert _counts(copy.deepcopy(opt)) == [5, 5, 5]
+
+
+def test_states_of_other_parameters_are_refused():
+    """The same number of blocks in all, other tensors: [300, 64] takes 2 + 1
+    blocks, [64, 300] 1 + 2."""
+    def opt(*sizes, **kw):
+        return qn.AdamW([torch.nn.Parameter(torch.ones(n)) for n in sizes], **kw)
+    for bits in (32, 8):
+        saved = opt(300, 64, bits=bits).state_dict()
+        opt(300, 64, bits=bits).load_state_dict(saved)
+        for other in (opt(64, 300, bits=bits), opt(301, 64, bits=bits), opt(256, 512, bits=bits)):
+            other._kept[0]["state"].m.fill_(3)
+            with pytest.raises(ValueError, match="other parameters"):
+                other.load_state_dict(saved)
+            assert (other._kept[0]["state"].m == 3).all()
+    # the same number of elements in another shape
+    a = qn.AdamW([torch.nn.Parameter(torch.ones(4, 75))])
+    with pytest.raises(ValueError, match="other parameters"):
+        a.load_state_dict(qn.AdamW([torch.nn.Parameter(torch.ones(75, 4))]).state_dict())
+    # states saved without the shapes: by their sizes in all
+    saved = opt(300, 64).state_dict()
+    del saved["kept"][0]["shapes"]
+    opt(300, 64).load_state_dict(saved)
+    with pytest.raises(ValueError, match="other parameters"):
+        opt(300, 640).load_state_dict(saved)
+
+
+def test_groups_are_counted():
+    ps = [torch.nn.Parameter(torch.ones(300)) for _ in range(2)]
+    opt = qn.AdamW([{"params": ps[:1], "lr": 0.5}, {"params": ps[1:], "lr": 0.25}])
+    for name in ("groups", "kept"):
+        saved = opt.state_dict()
+        saved[name] = saved[name][:1]
+        with pytest.raises(ValueError, match="groups"):
+            opt.load_state_dict(saved)
+        assert [g["lr"] for g in opt.param_groups] == [0.5, 0.25]
+
+
+def test_saved_states_are_plain(tmp_path):
+    """They pass through torch's file format without code."""
+    ps = [torch.nn.Parameter(torch.ones(4, 75)), torch.nn.Parameter(torch.ones(7).bfloat16())]
+    opt = qn.AdamW(ps, bits=8, masters=True, betas=(0.8, 0.9))
+    torch.save(opt.state_dict(), tmp_path / "s.pt")
+    saved = torch.load(tmp_path / "s.pt", weights_only=True)
+    other = qn.AdamW([torch.nn.Parameter(p.detach().clone()) for p in ps], bits=8, masters=True)
+    other.load_state_dict(saved)
+    assert other.param_groups[0]["betas"] == (0.8, 0.9)
