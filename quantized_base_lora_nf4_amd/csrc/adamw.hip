@@ -136,8 +136,8 @@ __device__ __forceinline__ float code_m(float y) {
   const float h = n + 0.5f;
   return h * h <= y ? h + 0.5f : n;
 }
-// low: the square root of y, less 2^-20 of it, within a few units (0 for y below
-// 2^-96: code 0 or 1).  Its root is 127 2^-20 below the code's at most.
+// low: the square root of y, less 2^-20 of it, within a few units (or 0 for a
+// subnormal value, whose y is below 4: code 0 or 1).  Its root is 127 2^-20 below the code's at most.
 __device__ __forceinline__ float code_v(float y, float low) {
 #pragma clang fp contract(off)
   const float n = rintf(__builtin_amdgcn_sqrtf(low));
@@ -231,8 +231,24 @@ struct Raw {
   }
 };
 
+// The square root of a second moment.  v_sqrt is within 1 ulp, far below the
+// parameter's rounding, but takes subnormal numbers as 0: kTiny scales them.
+template <bool kTiny>
+__device__ __forceinline__ float root_of(float v) {
+  if constexpr (!kTiny) return __builtin_amdgcn_sqrtf(v);
+  const bool low = v < 0x1p-96f;
+  return __builtin_amdgcn_sqrtf(low ? v * 0x1p64f : v) * (low ? 0x1p-32f : 1.0f);
+}
+
+// Whether that matters: a root of a subnormal number is below 2^-63, in the
+// denominator below 2^-63 / sqrt(1 - beta2) at any step, and nothing (half a
+// rounding of 2^-24) beside an eps of 2^-38 / sqrt(1 - beta2).  The usual eps of
+// 1e-8 is above that up to a beta2 of 1 - 1.4e-7.  (160 M bf16 elements in one
+// run, without and with it: 8-bit states 365 and 405 us, 32-bit ones 727 both.)
+bool tiny_matters(const AdamHyper& h) { return !(h.eps >= 0x1p-38 / sqrt(1.0 - h.beta2)); }
+
 // The step of one block.
-template <bool k8, class PT, class GT>
+template <bool k8, bool kTiny, class PT, class GT>
 __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, uint16_t* c,
                                              const State& st, int64_t blk, int count,
                                              const Step& s) {
@@ -275,10 +291,11 @@ __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, ui
         mtop = mtop > a ? mtop : a;
         vtop = vtop > b ? vtop : b;
       }
-      // v_sqrt and v_rcp are within 1 ulp: far below the parameter's rounding
-      root[j][i] = __builtin_amdgcn_sqrtf(v[j][i]);
+      root[j][i] = root_of<kTiny>(v[j][i]);
       const float d = root[j][i] * s.rb2 + s.eps;
-      pv[j][i] = pv[j][i] * s.keep - s.lr1 * m[j][i] * __builtin_amdgcn_rcpf(d);
+      // (v_rcp is within 1 ulp too, and takes subnormal numbers as 0 too)
+      if constexpr (kTiny) pv[j][i] = pv[j][i] * s.keep - s.lr1 * m[j][i] / d;
+      else pv[j][i] = pv[j][i] * s.keep - s.lr1 * m[j][i] * __builtin_amdgcn_rcpf(d);
     }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -332,7 +349,7 @@ __device__ __forceinline__ void update_block(const Raw<k8, PT, GT>& r, PT* p, ui
 // has `tail` elements.  With 32-bit states the next chunk's loads are in flight
 // under the arithmetic of this one (755 -> 722 us for 160 M bf16 elements); with
 // 8-bit ones the registers cost more than that (327 us against 302 for 115 M).
-template <bool k8, class PT, class GT>
+template <bool k8, bool kTiny, class PT, class GT>
 __device__ __forceinline__ void update_chunks(PT* p, const GT* g, uint16_t* c, const State& st,
                                               int64_t first, int64_t k0, int64_t k1, int64_t blocks,
                                               int tail, const Step& s) {
@@ -348,12 +365,12 @@ __device__ __forceinline__ void update_chunks(PT* p, const GT* g, uint16_t* c, c
     Raw<k8, PT, GT> n;
     if constexpr (k8) load_at(a, b);
     else load_at(n, b + kChunk);
-    update_block<k8>(a, p + b * kBlock, c ? c + b * kBlock : nullptr, st, first + b, size_of(b), s);
+    update_block<k8, kTiny>(a, p + b * kBlock, c ? c + b * kBlock : nullptr, st, first + b, size_of(b), s);
     if constexpr (!k8) a = n;
   }
 }
 
-template <bool k8, bool kCopy, class Tb>
+template <bool k8, bool kTiny, bool kCopy, class Tb>
 __global__ __launch_bounds__(kNT) void k_adamw(Tb tb, State st, AdamHyper hyper) {
   const Step s = step_of(hyper);
   const uint32_t total = tb.end[tb.n - 1];
@@ -379,16 +396,16 @@ __global__ __launch_bounds__(kNT) void k_adamw(Tb tb, State st, AdamHyper hyper)
     const int64_t first = tb.first[lo];
     switch (tail >> 30) {
       case 0:
-        update_chunks<k8>((uint16_t*)p, (const uint16_t*)g, c, st, first, k0, k1, blocks, last, s);
+        update_chunks<k8, kTiny>((uint16_t*)p, (const uint16_t*)g, c, st, first, k0, k1, blocks, last, s);
         break;
       case 1:
-        update_chunks<k8>((uint16_t*)p, (const float*)g, c, st, first, k0, k1, blocks, last, s);
+        update_chunks<k8, kTiny>((uint16_t*)p, (const float*)g, c, st, first, k0, k1, blocks, last, s);
         break;
       case 2:
-        update_chunks<k8>((float*)p, (const uint16_t*)g, c, st, first, k0, k1, blocks, last, s);
+        update_chunks<k8, kTiny>((float*)p, (const uint16_t*)g, c, st, first, k0, k1, blocks, last, s);
         break;
       default:
-        update_chunks<k8>((float*)p, (const float*)g, c, st, first, k0, k1, blocks, last, s);
+        update_chunks<k8, kTiny>((float*)p, (const float*)g, c, st, first, k0, k1, blocks, last, s);
     }
     ch = from + (uint32_t)k1;
   }
@@ -397,6 +414,7 @@ __global__ __launch_bounds__(kNT) void k_adamw(Tb tb, State st, AdamHyper hyper)
 template <class Tb, bool kCopy>
 hipError_t launch(const AdamArgs& a, int cap, hipStream_t stream) {
   const State st{a.m, a.v, a.ms, a.vs};
+  const bool tiny = tiny_matters(a.hyper);
   int64_t blk = 0;
   for (int64_t i = 0; i < a.n;) {
     Tb tb{};
@@ -421,8 +439,9 @@ hipError_t launch(const AdamArgs& a, int cap, hipStream_t stream) {
     }
     if (tb.n == 0) break;
     const dim3 grid(end < (uint32_t)kAdamGrid ? end : (uint32_t)kAdamGrid);
-    if (a.bits == 8) k_adamw<true, kCopy, Tb><<<grid, kNT, 0, stream>>>(tb, st, a.hyper);
-    else k_adamw<false, kCopy, Tb><<<grid, kNT, 0, stream>>>(tb, st, a.hyper);
+    auto* const k = a.bits == 8 ? (tiny ? &k_adamw<true, true, kCopy, Tb> : &k_adamw<true, false, kCopy, Tb>)
+                                : (tiny ? &k_adamw<false, true, kCopy, Tb> : &k_adamw<false, false, kCopy, Tb>);
+    k<<<grid, kNT, 0, stream>>>(tb, st, a.hyper);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
