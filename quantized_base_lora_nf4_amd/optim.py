@@ -298,18 +298,24 @@ class AdamW(torch.optim.Optimizer):
                 norm = self.last_norm = grad_norm(there)
         for group, kept, grads in zip(self.param_groups, self._kept, given):
             ps = group["params"]
-            if all(g is None for g in grads):
+            have, counts = [g is not None for g in grads], kept["step"]
+            if not any(have):
                 continue
+            if all(have) and counts.count(counts[0]) == len(counts):
+                step = counts[0] + 1
+                counts = [step] * len(counts)
+            else:
+                counts = [s + h for s, h in zip(counts, have)]
+                told = {s for s, h in zip(counts, have) if h}
+                step = counts if len(told) > 1 else told.pop()
             data, copies = [p.detach() for p in ps], None
             if kept["masters"] is not None:
                 copies = [None if m is None else p for p, m in zip(data, kept["masters"])]
                 data = [p if m is None else m for p, m in zip(data, kept["masters"])]
-            step = [s if g is None else s + 1 for s, g in zip(kept["step"], grads)]
-            told = {s for s, g in zip(step, grads) if g is not None}
-            adamw_step(data, grads, kept["state"], step if len(told) > 1 else told.pop(),
-                       group["lr"], group["betas"], group["eps"], group["weight_decay"], norm,
+            adamw_step(data, grads, kept["state"], step, group["lr"], group["betas"],
+                       group["eps"], group["weight_decay"], norm,
                        None if norm is None else self.max_norm, copies)
-            kept["step"] = step   # (a call that refuses has updated nothing)
+            kept["step"] = counts   # (a call that refuses has updated nothing)
         return loss
 
     def state_dict(self):
