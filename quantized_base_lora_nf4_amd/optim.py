@@ -261,10 +261,15 @@ class AdamW(torch.optim.Optimizer):
     def add_param_group(self, group) -> None:
         super().add_param_group(group)
         ps = self.param_groups[-1]["params"]
-        masters = [p.detach().float() if p.dtype == torch.bfloat16 else None for p in ps] \
-            if self.use_masters else None
-        self._kept.append({"state": adamw_init(ps, self.bits), "masters": masters,
-                           "step": [0] * len(ps)})
+        try:
+            masters = [p.detach().float() if p.dtype == torch.bfloat16 else None for p in ps] \
+                if self.use_masters else None
+            # (a group without parameters has empty states)
+            state = adamw_init(ps, self.bits, ps[0].device if ps else "cpu")
+        except BaseException:   # no memory
+            self.param_groups.pop()
+            raise
+        self._kept.append({"state": state, "masters": masters, "step": [0] * len(ps)})
 
     @torch.no_grad()
     def take_masters(self) -> None:

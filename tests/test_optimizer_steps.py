@@ -135,3 +135,29 @@ def test_saved_states_are_plain(tmp_path):
     other = qn.AdamW([torch.nn.Parameter(p.detach().clone()) for p in ps], bits=8, masters=True)
     other.load_state_dict(saved)
     assert other.param_groups[0]["betas"] == (0.8, 0.9)
+
+
+def test_groups_without_parameters(monkeypatch):
+    """As torch's optimizers: such a group is there, and has nothing to do."""
+    monkeypatch.setattr(optim, "adamw_step", lambda *a, **k: None)
+    ps, opt = _opt(1, bits=8, masters=True)
+    opt.add_param_group({"params": [], "lr": 0.5})
+    ps[0].grad = torch.ones_like(ps[0])
+    opt.step()
+    opt.take_masters()
+    saved = opt.state_dict()
+    assert [k["step"] for k in saved["kept"]] == [[1], []]
+    opt.param_groups[1]["lr"] = 0.25
+    opt.load_state_dict(saved)
+    assert opt.param_groups[1]["lr"] == 0.5
+
+
+def test_a_group_that_fails_is_not_added(monkeypatch):
+    ps, opt = _opt(1)
+
+    def no_room(*a):
+        raise MemoryError
+    monkeypatch.setattr(optim, "adamw_init", no_room)
+    with pytest.raises(MemoryError):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.ones(3))]})
+    assert len(opt.param_groups) == len(opt._kept) == 1
