@@ -351,10 +351,22 @@ int32_t qlora_linear_fwd_noalloc(const nf4_tensor_t* w, const uint16_t* X,
  *                each other (prompts) cost least.  Read by the kernels; any
  *                value is allowed.
  *   ws           >= qlora_multi_workspace_size(M, N, K, r) bytes
- * M <= 16 streams the packed weight once, as qlora_linear_fwd does; larger M
- * takes the MFMA tile path.  A row's result does not depend on adapters that
- * it does not have, whatever they hold; an infinity or NaN in B gives its
- * adapter's rows an infinity or NaN in that column. */
+ * Three kernels, chosen by M, N, K and r alone: M <= 16 streams the packed weight
+ * once, as qlora_linear_fwd does, while the tables of a workgroup fit its LDS
+ * (K up to about 32000 at rank 256); otherwise batches of up to a few hundred
+ * rows, 4096 at most, stream it with up to 64 tokens per workgroup, where that is
+ * estimated to be the faster way; the rest takes the MFMA tile path.  So a row's
+ * last bits depend on how many rows come with it, though not on which ones.
+ * Besides the one rounding of Y to bf16, and sums in fp32:
+ *   both streams   a weight is its level rounded to bf16 (after a common factor
+ *                  that brings the levels nearer to bf16 values) times an fp32
+ *                  constant, where the tiles, as nf4_dequantize, round level times
+ *                  constant; X A^T stays in fp32
+ *   tiles          s (X A^T) is rounded to bf16 once (qlora_linear_fwd rounds
+ *                  X A^T and s times that)
+ * A row's result does not depend on adapters that it does not have, whatever
+ * they hold; an infinity or NaN in B gives its adapter's rows an infinity or NaN
+ * in that column. */
 size_t qlora_multi_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r);
 int32_t qlora_linear_multi_fwd(const nf4_tensor_t* w, const uint16_t* X, int64_t M,
                                const uint16_t* A, const uint16_t* B, const float* s,

@@ -327,7 +327,7 @@ __device__ __forceinline__ void store_at(uint16_t* out, int64_t ld, const int* a
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-      // (all 64 addresses at once spill)
+      // (all 64 addresses at once would spill here)
       if (v % 4 == 0) __builtin_amdgcn_sched_barrier(0);
       const int row = at[wm * C::FM * 32 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)];
       if (row < 0) continue;
@@ -451,6 +451,11 @@ struct MultiFwdArgs : FwdArgs {
 // step takes 8 units, so that 8 adapters of rank 8 cost what one of rank 64
 // does, and rows need no order (256 rows of 64 adapters of rank 16: 16 steps
 // beside the 64 of K = 4096; in runs of rows, one or two).
+// s U is rounded to bf16 to be an MFMA operand: one rounding, where the tiles for
+// one adapter make two (U, then s U).  Two operands (the value and what its
+// rounding leaves) would keep it, for twice the contraction steps.  It makes the
+// error against 64 bits 2.3e-3 of the norm instead of 1.66e-3, which Y's own
+// rounding leaves, where the adapters' term is the larger part of Y.
 // Zero times an infinity or NaN of another row's adapter would not be zero:
 // such elements of B are staged as zeros and noted, by adapter and column,
 // and the adapter's own rows get NaN in those columns at the end.
@@ -519,7 +524,9 @@ __device__ __forceinline__ void multi_lora(const MultiFwdArgs& p, uint16_t* As, 
     const bool in = q0 + c8 < total;
     const int ai = in ? (q0 + c8) / units : 0, j = in ? 8 * (q0 + c8 - ai * units) : 0;
     // U: rows of other adapters read what is there and drop it.  (Loads behind
-    // branches, or more of them at once, spill the accumulators.)
+    // branches, or more of them at once, spill the accumulators in this loop.  As
+    // it is the 256 x 256 tiles keep 80 bytes per lane in scratch, moved before the
+    // main loop and in the branch for infinities and NaN; the smaller tiles none.)
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       __builtin_amdgcn_sched_barrier(0);

@@ -5,7 +5,9 @@
 //
 // As in gemv.hip a workgroup owns 16 G weight rows and all of K, its 8 waves
 // split K, codes are expanded to unscaled bf16 levels by a byte-indexed table
-// in LDS, and the block constant multiplies each 64-element block's fp32 sum.
+// in LDS, and the block constant multiplies each 64-element block's fp32 sum:
+// the levels' rounding (6e-4 of a weight, level_factor) takes the place of the
+// dequantized weight's (1.7e-3), and X A^T is not rounded.
 // Here up to 16 T tokens share the expanded codes: T MFMA column tiles per
 // code word.  Every workgroup reads all of X (from L2; G = 4 halves that
 // traffic), so it comes in the order of the MFMA operands, 1 KB per load, as
@@ -398,7 +400,9 @@ struct Shape {
 int64_t over(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The tile and its time, from the shapes alone: the rounds of workgroups over
-// 256 compute units times a workgroup's time.  Measured with 24 adapters of
+// 256 compute units times a workgroup's time.  (The whole chip's, to which the
+// constants are fitted: the workspace's size follows from this choice and is the
+// same wherever it is asked for.)  Measured with 24 adapters of
 // rank 32, us a call, G = 2 / G = 4: 64 rows over 8192 x 8192 37 / 47, 128 rows
 // 58 / 48, 256 rows 100 / 79; 64 over 11008 x 4096 40 / 34; 64 over 28672 x 8192
 // 106 / 83.  Up to 32 rows: 17 over 11008 x 4096 29.7 / 24.6, over 28672 x 8192

@@ -24,9 +24,11 @@ def qlora_linear_multi_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: to
     Y_i = X_i W^T + s_a (X_i A_a^T) B_a^T with a = index[i], and X_i W^T where
     index[i] is not one of 0 .. n - 1.
 
-    X [M, K], A [n, r, K], B [n, N, r] bf16 (adapters of smaller rank padded
-    with zeros), s [n] float32, index [M] int32, all on the weight's GPU.  Rows
-    may come in any order; Y overlaps nothing that is read."""
+    X [M, K] (M at least 1), A [n, r, K], B [n, N, r] bf16 (adapters of smaller
+    rank padded with zeros), s [n] float32, index [M] int32, all on the weight's
+    GPU.  Rows may come in any order; Y overlaps nothing that is read.  M, N, K
+    and r choose the kernel, and with it where bf16 is rounded to (see the C
+    header): a row's last bits depend on how many rows come with it."""
     dev = _check_weight(w)
     if dev.type != "cuda":
         raise ValueError(f"codes is on {dev}, expected a GPU")
@@ -100,8 +102,8 @@ class QLoRAMultiLinear(torch.nn.Module):
 
     @torch.no_grad()
     def forward(self, X, index):
-        """X [..., K] bf16, index int32 of X's leading shape: the slot of each
-        row, -1 for none."""
+        """X [..., K] bf16 of one row or more, index int32 of X's leading shape:
+        the slot of each row, -1 for none."""
         shp = X.shape
         Y = qlora_linear_multi_fwd(self.nf4, X.reshape(-1, shp[-1]).contiguous(), self.A, self.B,
                                    self.scales, index.reshape(-1).contiguous())
